@@ -385,6 +385,116 @@ int moe_layer_backward(const moe_problem_t* p, const void* x, const moe_weights_
                        const void* dy, float d_loss, float d_zloss, const moe_grads_t* grads,
                        void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The layer for a few tokens.
+ *
+ * moe_layer_forward for 1 <= T <= MOE_FEW_MAX_TOKENS tokens in ONE kernel
+ * (cooperative launch), for decode steps and other small batches: the experts'
+ * weights are streamed once, without the gaps between the six launches of
+ * moe_layer_forward.  Same arguments, outputs, conventions and errors as
+ * moe_layer_forward, except
+ *   - ws: moe_few_workspace_size bytes, 256-byte aligned; any contents.  The
+ *     status word is its first word, as everywhere, and is reset by the call;
+ *   - logits are summed in FP32 and FP64, expert outputs stay in FP32 up to
+ *     the combine (moe_layer_forward rounds them to the activations' type
+ *     first), so the two entry points agree to rounding, not bit for bit.
+ *     Results of one entry point repeat bit for bit;
+ *   - MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_TOKENS, or a d_model whose row
+ *     of weights exceeds 69568 bytes (34784 for BF16, 17392 for FP32, 69568
+ *     for 8-bit weights);
+ *   - MOE_FLAG_SAVE_GU is MOE_ERR_INVALID_ARG: this is the serving forward, the
+ *     backward reads the workspace of moe_layer_forward.
+ * The kernel's blocks wait on one another: the device must be able to hold one
+ * of them per SM (the launch fails with MOE_ERR_CUDA otherwise). */
+#define MOE_FEW_MAX_TOKENS 64
+int moe_few_workspace_size(const moe_problem_t* p, size_t* bytes);
+int moe_layer_forward_few(const moe_problem_t* p, const void* x, const moe_weights_t* w,
+                          void* y, const moe_routing_t* routing, float* stats,
+                          void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit integers.
+ *
+ * A row v is held as int8 q and one FP32 scale s:
+ *   s = max(fl32(max|v| / 127), 2^-126),  q = the integer nearest to v / s
+ * (of the real quotient, ties to even), -127 <= q <= 127, v ~ q s.  A row with
+ * an infinity or a NaN gets s = NaN, q = 0: whatever is computed from it is
+ * NaN, other rows are not touched.
+ * A product of rows x (a scale per row) and weights w (a scale per output
+ * channel) is
+ *   y[r, n] = (sum_k xq[r, k] wq[n, k]) * (xs[r] * ws[n])
+ * with the sum exact in int32 (reductions up to 131056, so that even 128 * 128
+ * per term cannot overflow) and the scaling in FP32.
+ *
+ * Weights are quantised with the same rule: moe_quantize_rows over the E * 2F
+ * rows of w13 and the E * d rows of w2.  The shared experts count as ONE expert
+ * of width N_s * F: their hidden row has one scale per token, and w2_shared one
+ * per output channel over all N_s * F inputs.  Inference only: there is no
+ * backward through the rounding. */
+
+/* Rows to 8 bits.  x [n_rows, n_cols] of `dtype` (moe_dtype) -> x_q
+ * [n_rows, n_cols], x_scale [n_rows].  n_cols a multiple of 16; pointers
+ * 16-byte aligned.  No workspace. */
+int moe_quantize_rows(int64_t n_rows, int32_t n_cols, int32_t dtype, const void* x,
+                      int8_t* x_q, float* x_scale, moe_stream_t stream);
+
+/* Grouped matrix product on 8-bit integers.
+ *   x [n_rows, K], x_scale [n_rows]; w [n_groups, N, K], w_scale [n_groups, N];
+ *   seg_off [n_groups + 1] int32: rows [seg_off[g], seg_off[g+1]) meet w[g]
+ *   (non-decreasing, clamped to [0, n_rows]; rows of no group are left as they
+ *   were in y).  NULL with n_groups == 1: all rows;
+ *   y [n_rows, N] BF16 or FP32 (out_dtype, a moe_dtype);
+ *   ws: MOE_MATMUL_WORKSPACE bytes, 256-byte aligned: the device status word
+ *   (zero it once: moe_reset_device_status).
+ * K a multiple of 16, N of 8; n_groups <= 256, K <= 131056 (else
+ * MOE_ERR_UNSUPPORTED). */
+#define MOE_MATMUL_WORKSPACE 256
+int moe_matmul_i8(int32_t n_groups, int64_t n_rows, int32_t N, int32_t K, const int8_t* x,
+                  const float* x_scale, const int32_t* seg_off, const int8_t* w, const float* w_scale,
+                  int32_t out_dtype, void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Workspace of moe_expert_ffn_i8 and moe_layer_forward_i8 for problem p. */
+int moe_i8_workspace_size(const moe_problem_t* p, size_t* bytes);
+
+/* moe_expert_ffn on 8-bit rows and weights: h = silu(g) * u in FP32, each
+ * hidden row to 8 bits by the rule above, the down product to BF16 rows.
+ *   x_rows [n_rows, d], x_scale [n_rows] (moe_quantize_rows);
+ *   w13 [E, 2F, d], w13_scale [E, 2F]; w2 [E, d, F], w2_scale [E, d];
+ *   mode MOE_FFN_SHARED: w13 [N_s, 2F, d], w13_scale [N_s, 2F], w2 [N_s, d, F],
+ *   w2_scale [d]; y_rows [n_rows, d] BF16.
+ * seg_off, n_rows, row ranges and errors as moe_expert_ffn.  BF16 problems
+ * (FP32: MOE_ERR_UNSUPPORTED); d_model and d_ff multiples of 16, d_model and
+ * max(N_s, 1) * d_ff at most 131056. */
+int moe_expert_ffn_i8(const moe_problem_t* p, int32_t mode, const int8_t* x_rows, const float* x_scale,
+                      int64_t n_rows, const int32_t* seg_off, const int8_t* w13, const float* w13_scale,
+                      const int8_t* w2, const float* w2_scale, void* y_rows,
+                      void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Weights of a layer with 8-bit experts; the router keeps the activations' type. */
+typedef struct moe_weights_i8 {
+    const void* w_gate;        /* [E, d] BF16; unused with MOE_FLAG_LOGITS_GIVEN */
+    const float* logit_offset; /* [E] or NULL */
+    const float* sel_bias;     /* [E] or NULL */
+    const int8_t* w13;         /* [E, 2F, d] */
+    const float* w13_scale;    /* [E, 2F] */
+    const int8_t* w2;          /* [E, d, F] */
+    const float* w2_scale;     /* [E, d] */
+    const int8_t* w13_shared;  /* [N_s, 2F, d]; the four shared ones NULL iff n_shared == 0 */
+    const float* w13_shared_scale; /* [N_s, 2F] */
+    const int8_t* w2_shared;   /* [N_s, d, F] */
+    const float* w2_shared_scale;  /* [d] */
+    const int32_t* expert_capacity; /* as in moe_weights_t */
+} moe_weights_i8_t;
+
+/* moe_layer_forward with 8-bit experts (any T; ws of moe_i8_workspace_size),
+ * and moe_layer_forward_few with them (ws of moe_few_workspace_size). */
+int moe_layer_forward_i8(const moe_problem_t* p, const void* x, const moe_weights_i8_t* w,
+                         void* y, const moe_routing_t* routing, float* stats,
+                         void* ws, size_t ws_bytes, moe_stream_t stream);
+int moe_layer_forward_few_i8(const moe_problem_t* p, const void* x, const moe_weights_i8_t* w,
+                             void* y, const moe_routing_t* routing, float* stats,
+                             void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Stage boundaries recorded by moe_layer_forward_profiled. */
 #define MOE_EV_START 0   /* before the router */
 #define MOE_EV_ROUTED 1  /* after gate logits, selection and statistics */

@@ -30,7 +30,11 @@ EXPORTED = ("moe_abi_version", "moe_status_string", "moe_capacity", "moe_max_row
             "moe_layer_forward_clocked", "moe_expert_ffn_segments",
             "moe_dispatch_noalloc", "moe_dispatch_capacity", "moe_balance_update", "moe_backward_workspace_size",
             "moe_layer_backward", "moe_ep_plan", "moe_ep_peer_plan", "moe_ep_scatter", "moe_ep_combine",
-            "moe_ipc_malloc", "moe_ipc_free", "moe_ipc_handle", "moe_ipc_open", "moe_ipc_close")
+            "moe_ipc_malloc", "moe_ipc_free", "moe_ipc_handle", "moe_ipc_open", "moe_ipc_close",
+            "moe_few_workspace_size", "moe_layer_forward_few", "moe_quantize_rows", "moe_matmul_i8",
+            "moe_i8_workspace_size", "moe_expert_ffn_i8", "moe_layer_forward_i8", "moe_layer_forward_few_i8")
+FEW_MAX_TOKENS = 64
+MATMUL_WORKSPACE = 256
 NUM_EVENTS = 7  # MOE_EV_START .. MOE_EV_END
 EVENT_NAMES = ("start", "routed", "dispatched", "up", "down", "shared", "end")
 NUM_CLOCKS = 7  # MOE_CLOCK_ROUTE .. MOE_CLOCK_COMBINE
@@ -48,6 +52,14 @@ class MoeWeights(ctypes.Structure):
     _fields_ = [("w_gate", ctypes.c_void_p), ("logit_offset", ctypes.c_void_p), ("sel_bias", ctypes.c_void_p),
                 ("w13", ctypes.c_void_p), ("w2", ctypes.c_void_p), ("w13_shared", ctypes.c_void_p),
                 ("w2_shared", ctypes.c_void_p), ("expert_capacity", ctypes.c_void_p)]
+
+
+class MoeWeightsI8(ctypes.Structure):
+    _fields_ = [("w_gate", ctypes.c_void_p), ("logit_offset", ctypes.c_void_p), ("sel_bias", ctypes.c_void_p),
+                ("w13", ctypes.c_void_p), ("w13_scale", ctypes.c_void_p), ("w2", ctypes.c_void_p),
+                ("w2_scale", ctypes.c_void_p), ("w13_shared", ctypes.c_void_p), ("w13_shared_scale", ctypes.c_void_p),
+                ("w2_shared", ctypes.c_void_p), ("w2_shared_scale", ctypes.c_void_p),
+                ("expert_capacity", ctypes.c_void_p)]
 
 
 class MoeRouting(ctypes.Structure):
@@ -137,6 +149,21 @@ def lib() -> ctypes.CDLL:
     L.moe_ipc_open.restype = ctypes.c_int
     L.moe_ipc_close.argtypes = [P]
     L.moe_ipc_close.restype = ctypes.c_int
+    L.moe_few_workspace_size.argtypes = [PP, ctypes.POINTER(sz)]
+    L.moe_few_workspace_size.restype = ctypes.c_int
+    L.moe_layer_forward_few.argtypes = [PP, P, ctypes.POINTER(MoeWeights), P, ctypes.POINTER(MoeRouting), P, P, sz, P]
+    L.moe_layer_forward_few.restype = ctypes.c_int
+    L.moe_quantize_rows.argtypes = [i64, i32, i32, P, P, P, P]
+    L.moe_quantize_rows.restype = ctypes.c_int
+    L.moe_matmul_i8.argtypes = [i32, i64, i32, i32, P, P, P, P, P, i32, P, P, sz, P]
+    L.moe_matmul_i8.restype = ctypes.c_int
+    L.moe_i8_workspace_size.argtypes = [PP, ctypes.POINTER(sz)]
+    L.moe_i8_workspace_size.restype = ctypes.c_int
+    L.moe_expert_ffn_i8.argtypes = [PP, i32, P, P, i64, P, P, P, P, P, P, P, sz, P]
+    L.moe_expert_ffn_i8.restype = ctypes.c_int
+    for fn in (L.moe_layer_forward_i8, L.moe_layer_forward_few_i8):
+        fn.argtypes = [PP, P, ctypes.POINTER(MoeWeightsI8), P, ctypes.POINTER(MoeRouting), P, P, sz, P]
+        fn.restype = ctypes.c_int
     if L.moe_abi_version() != ABI_VERSION:
         raise RuntimeError(f"{LIB_PATH} has ABI version {L.moe_abi_version()}, this binding expects {ABI_VERSION}: "
                            "rebuild it")

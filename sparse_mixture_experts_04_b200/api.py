@@ -14,7 +14,8 @@ from . import _lib
 from ._lib import (BIAS_UPDATE_PROPORTIONAL, BIAS_UPDATE_SIGN, DTYPE_BF16, DTYPE_F32, EXTENDED_STATS, FFN_ROUTED,
                    FFN_SHARED, FLAG_BIAS_LOGIT, FLAG_EXPERT_CAPACITY, FLAG_EXTENDED_STATS, FLAG_LOGITS_GIVEN,
                    FLAG_SAVE_GU,
-                   MoeError, MoeGrads, MoeProblem, MoeRouting, MoeWeights)
+                   FEW_MAX_TOKENS, MATMUL_WORKSPACE,
+                   MoeError, MoeGrads, MoeProblem, MoeRouting, MoeWeights, MoeWeightsI8)
 
 __all__ = ["MoeError", "MoeProblem", "make_problem", "workspace_size", "capacity", "max_rows", "alloc_workspace",
            "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_expert_ffn_segments", "moe_combine", "moe_layer_forward",
@@ -23,7 +24,10 @@ __all__ = ["MoeError", "MoeProblem", "make_problem", "workspace_size", "capacity
            "reset_device_status", "read_device_status", "FLAG_LOGITS_GIVEN", "FLAG_BIAS_LOGIT",
            "FLAG_EXTENDED_STATS", "FLAG_EXPERT_CAPACITY", "FLAG_SAVE_GU", "EXTENDED_STATS", "stats_size",
            "BIAS_UPDATE_SIGN", "BIAS_UPDATE_PROPORTIONAL",
-           "FFN_ROUTED", "FFN_SHARED", "DTYPE_BF16", "DTYPE_F32"]
+           "FFN_ROUTED", "FFN_SHARED", "DTYPE_BF16", "DTYPE_F32", "FEW_MAX_TOKENS", "few_workspace_size",
+           "alloc_few_workspace", "moe_layer_forward_few", "moe_layer_forward_few_i8", "quantize_rows",
+           "moe_quantize_rows", "moe_matmul_i8", "alloc_matmul_workspace", "i8_workspace_size", "alloc_i8_workspace",
+           "moe_expert_ffn_i8", "moe_layer_forward_i8"]
 
 
 def make_problem(T, d_model, n_experts, top_k, d_ff, n_shared=0, capacity_factor=0.0, dtype="bf16", flags=0,
@@ -253,6 +257,187 @@ def moe_ep_plan(n_ranks: int, rank: int, n_experts: int, seg_off_all) -> tuple:
     rc = _lib.lib().moe_ep_plan(G, int(rank), E, so.data_ptr(), send.data_ptr(), recv.data_ptr(), local.data_ptr())
     _lib.check("moe_ep_plan", rc)
     return send[:G], recv[:G], local
+
+
+# ------------------------------------------------- few tokens and 8-bit integers
+def _need(name: str, t: torch.Tensor, shape, dtype, device) -> None:
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _need_ws(ws: torch.Tensor, device) -> None:
+    if ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous uint8 tensor on {device}")
+
+
+def _cuda(name: str, t: torch.Tensor) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
+    return t.device
+
+
+class _on:
+    """Makes `device` current for a call (its launches and attributes are the
+    current device's) and gives the stream handle: `stream`, or that device's
+    current stream."""
+
+    def __init__(self, device: torch.device, stream):
+        self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
+        self.device, self.stream = device, stream
+
+    def __enter__(self) -> int:
+        if self.guard is not None:
+            self.guard.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream if self.stream is None else _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+_ACT_DTYPE = {DTYPE_BF16: torch.bfloat16, DTYPE_F32: torch.float32}
+_ACT_CODE = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+
+def few_workspace_size(prob: MoeProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _lib.check("moe_few_workspace_size", _lib.lib().moe_few_workspace_size(ctypes.byref(prob), ctypes.byref(n)))
+    return int(n.value)
+
+
+def alloc_few_workspace(prob: MoeProblem, device="cuda") -> torch.Tensor:
+    return torch.zeros(few_workspace_size(prob), dtype=torch.uint8, device=device)
+
+
+def i8_workspace_size(prob: MoeProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _lib.check("moe_i8_workspace_size", _lib.lib().moe_i8_workspace_size(ctypes.byref(prob), ctypes.byref(n)))
+    return int(n.value)
+
+
+def alloc_i8_workspace(prob: MoeProblem, device="cuda") -> torch.Tensor:
+    return torch.zeros(i8_workspace_size(prob), dtype=torch.uint8, device=device)
+
+
+def alloc_matmul_workspace(device="cuda") -> torch.Tensor:
+    return torch.zeros(MATMUL_WORKSPACE, dtype=torch.uint8, device=device)
+
+
+def _weights_i8_struct(w: dict) -> MoeWeightsI8:
+    return MoeWeightsI8(_p(w.get("w_gate")), _p(w.get("logit_offset")), _p(w.get("sel_bias")), _p(w["w13"]),
+                        _p(w["w13_scale"]), _p(w["w2"]), _p(w["w2_scale"]), _p(w.get("w13_shared")),
+                        _p(w.get("w13_shared_scale")), _p(w.get("w2_shared")), _p(w.get("w2_shared_scale")),
+                        _p(w.get("expert_capacity")))
+
+
+def _layer_call(name: str, prob, x, w_struct, y, routing, stats, ws, stream):
+    dev = _cuda("x", x)
+    shape, dt = (prob.T, prob.d_model), _ACT_DTYPE.get(prob.dtype, torch.bfloat16)
+    _need("x", x, shape, dt, dev)
+    _need("y", y, shape, dt, dev)
+    _need_ws(ws, dev)
+    r = _routing_struct(routing)
+    with _on(dev, stream) as st:
+        rc = getattr(_lib.lib(), name)(ctypes.byref(prob), _p(x), ctypes.byref(w_struct), _p(y),
+                                       ctypes.byref(r) if r is not None else None, _p(stats), _p(ws), ws.numel(), st)
+    _lib.check(name, rc)
+
+
+def moe_layer_forward_few(prob, x, weights: dict, y, routing: dict | None, stats, ws, stream=None):
+    """moe_layer_forward for at most FEW_MAX_TOKENS tokens, in one kernel; ws
+    from alloc_few_workspace."""
+    _layer_call("moe_layer_forward_few", prob, x, _weights_struct(weights), y, routing, stats, ws, stream)
+
+
+def moe_layer_forward_few_i8(prob, x, weights: dict, y, routing: dict | None, stats, ws, stream=None):
+    """moe_layer_forward_few with 8-bit experts (weights as moe_layer_forward_i8)."""
+    _layer_call("moe_layer_forward_few_i8", prob, x, _weights_i8_struct(weights), y, routing, stats, ws, stream)
+
+
+def moe_layer_forward_i8(prob, x, weights: dict, y, routing: dict | None, stats, ws, stream=None):
+    """moe_layer_forward with 8-bit experts: weights maps w13, w2 (int8),
+    w13_scale [E, 2F], w2_scale [E, d], the shared ones with their scales
+    ([N_s, 2F], [d]), w_gate and the optional arrays; ws from alloc_i8_workspace."""
+    _layer_call("moe_layer_forward_i8", prob, x, _weights_i8_struct(weights), y, routing, stats, ws, stream)
+
+
+def moe_quantize_rows(x, x_q, x_scale, stream=None):
+    """Rows of x [..., n] (BF16 or FP32) to int8 x_q (same shape) and one FP32
+    scale each, x_scale x.shape[:-1]."""
+    dev = _cuda("x", x)
+    if x.dtype not in _ACT_CODE:
+        raise ValueError(f"x must be BF16 or FP32, got {x.dtype}")
+    if x.dim() < 1 or not x.is_contiguous():
+        raise ValueError("x must be contiguous, with at least one dimension")
+    _need("x_q", x_q, x.shape, torch.int8, dev)
+    _need("x_scale", x_scale, x.shape[:-1], torch.float32, dev)
+    n = x.shape[-1]
+    with _on(dev, stream) as st:
+        rc = _lib.lib().moe_quantize_rows(x.numel() // n if n else 0, n, _ACT_CODE[x.dtype], _p(x), _p(x_q),
+                                          _p(x_scale), st)
+    _lib.check("moe_quantize_rows", rc)
+
+
+def quantize_rows(x: torch.Tensor, stream=None) -> tuple:
+    """(x_q, x_scale) of moe_quantize_rows in new tensors."""
+    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    s = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    moe_quantize_rows(x, q, s, stream)
+    return q, s
+
+
+def moe_matmul_i8(x_q, x_scale, seg_off, w, w_scale, y, ws, stream=None):
+    """y[r] = (x_q[r] . w[g]^T) * x_scale[r] * w_scale[g] for the rows of group
+    g, [seg_off[g], seg_off[g+1]); w [G, N, K] int8, w_scale [G, N] (or [N, K]
+    and [N] with seg_off None: every row); y [n_rows, N] BF16 or FP32; ws from
+    alloc_matmul_workspace."""
+    dev = _cuda("x_q", x_q)
+    if w.dim() not in (2, 3) or x_q.dim() != 2:
+        raise ValueError("x_q must be [n_rows, K] and w [G, N, K] or [N, K]")
+    G = w.shape[0] if w.dim() == 3 else 1
+    N, K = w.shape[-2], w.shape[-1]
+    rows = x_q.shape[0]
+    if y.dtype not in _ACT_CODE:
+        raise ValueError(f"y must be BF16 or FP32, got {y.dtype}")
+    _need("x_q", x_q, (rows, K), torch.int8, dev)
+    _need("x_scale", x_scale, (rows,), torch.float32, dev)
+    _need("w", w, w.shape, torch.int8, dev)
+    _need("w_scale", w_scale, w.shape[:-1], torch.float32, dev)
+    _need("y", y, (rows, N), y.dtype, dev)
+    _need_ws(ws, dev)
+    if seg_off is not None:
+        _need("seg_off", seg_off, (G + 1,), torch.int32, dev)
+    with _on(dev, stream) as st:
+        rc = _lib.lib().moe_matmul_i8(G, rows, N, K, _p(x_q), _p(x_scale), _p(seg_off), _p(w), _p(w_scale),
+                                      _ACT_CODE[y.dtype], _p(y), _p(ws), ws.numel(), st)
+    _lib.check("moe_matmul_i8", rc)
+
+
+def moe_expert_ffn_i8(prob, mode, x_q, x_scale, seg_off, w13, w13_scale, w2, w2_scale, y_rows, ws, stream=None):
+    """moe_expert_ffn on 8-bit rows and weights (see the header): x_q [n_rows, d],
+    x_scale [n_rows] from moe_quantize_rows; w13 [E, 2F, d], w13_scale [E, 2F],
+    w2 [E, d, F], w2_scale [E, d] (FFN_SHARED: N_s experts, w2_scale [d],
+    seg_off None); y_rows [n_rows, d] BF16; ws from alloc_i8_workspace."""
+    dev = _cuda("x_q", x_q)
+    d, F = prob.d_model, prob.d_ff
+    G = prob.n_shared if mode == FFN_SHARED else prob.n_experts
+    rows = x_q.shape[0] if x_q.dim() == 2 else -1
+    _need("x_q", x_q, (rows, d), torch.int8, dev)
+    _need("x_scale", x_scale, (rows,), torch.float32, dev)
+    _need("w13", w13, (G, 2 * F, d), torch.int8, dev)
+    _need("w13_scale", w13_scale, (G, 2 * F), torch.float32, dev)
+    _need("w2", w2, (G, d, F), torch.int8, dev)
+    _need("w2_scale", w2_scale, (d,) if mode == FFN_SHARED else (G, d), torch.float32, dev)
+    _need("y_rows", y_rows, (rows, d), torch.bfloat16, dev)
+    _need_ws(ws, dev)
+    if mode != FFN_SHARED and seg_off is not None:
+        _need("seg_off", seg_off, (G + 1,), torch.int32, dev)
+    with _on(dev, stream) as st:
+        rc = _lib.lib().moe_expert_ffn_i8(ctypes.byref(prob), int(mode), _p(x_q), _p(x_scale), rows, _p(seg_off),
+                                          _p(w13), _p(w13_scale), _p(w2), _p(w2_scale), _p(y_rows), _p(ws),
+                                          ws.numel(), st)
+    _lib.check("moe_expert_ffn_i8", rc)
 
 
 # ----------------------------------------------------- expert parallel over peer memory

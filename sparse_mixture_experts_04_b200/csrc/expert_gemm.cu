@@ -40,10 +40,21 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "quant.cuh"
 
 namespace moe {
 
-enum { EPI_SWIGLU = 0, EPI_BF16 = 1, EPI_F32 = 2 };
+// EPI_I8_SWIGLU and EPI_I8_OUT: the operands are 8-bit integers with a scale per
+// row of A and per row of B (tcgen05.mma kind::i8, exact int32 sums).  The byte
+// geometry is that of BF16: a 128-byte swizzle row holds 128 integers instead
+// of 64 BF16, an MMA reduces 32 bytes of each operand, so the tensor maps view
+// two neighbouring integers as one 2-byte element and K counts those pairs.
+//   EPI_I8_SWIGLU : h = silu(g) * u as FP32 rows, and each row's largest |h|
+//                   (its 8-bit scale needs the whole row, which no tile has)
+//   EPI_I8_OUT    : y = (sum) * a_scale[row] * b_scale[column], BF16 or FP32
+enum { EPI_SWIGLU = 0, EPI_BF16 = 1, EPI_F32 = 2, EPI_I8_SWIGLU = 3, EPI_I8_OUT = 4 };
+__host__ __device__ constexpr bool is_i8(int epi) { return epi == EPI_I8_SWIGLU || epi == EPI_I8_OUT; }
+__host__ __device__ constexpr bool is_swiglu(int epi) { return epi == EPI_SWIGLU || epi == EPI_I8_SWIGLU; }
 
 constexpr int kBM = 128;
 constexpr int kBK = 64;  // 64 BF16 = 128 bytes: one 128-byte swizzle row
@@ -93,6 +104,15 @@ struct GemmArgs {
   // segments that repeat the experts, e.g. one run of experts per source rank
   // in the expert-parallel receive buffer); 0: expert g
   int weight_mod;
+  // 8-bit epilogues: scale of each row of A and of each B row (group g's at
+  // b_scale + g * b_scale_stride; EPI_I8_SWIGLU: N gate scales, then N up
+  // scales), the bits of each output row's largest magnitude (EPI_I8_SWIGLU,
+  // raised with atomicMax), and the output type (EPI_I8_OUT: 1 FP32, 0 BF16)
+  const float* a_scale;
+  const float* b_scale;
+  int64_t b_scale_stride;
+  unsigned* row_amax;
+  int out_f32;
 };
 
 // Reduction range of a tile of group g: first k, number of 64-wide k-blocks.
@@ -109,7 +129,7 @@ __device__ __forceinline__ void tile_k_range(const GemmArgs& a, int g, int* k0, 
 
 template <int EPI, int BN>
 struct TileCfg {
-  static constexpr int kOutCols = (EPI == EPI_SWIGLU) ? BN / 2 : BN;
+  static constexpr int kOutCols = is_swiglu(EPI) ? BN / 2 : BN;
   static constexpr int kABytes = kBM * kBK * 2;
   static constexpr int kBBytes = BN * kBK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
@@ -223,6 +243,29 @@ __device__ __forceinline__ TileInfo decode_mixed_tile(int tile, int t1, int tota
   return ti;
 }
 
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// silu(g) * u from int32 sums: the sum times (row scale * column scale) in
+// FP32, three roundings per factor.
+__device__ __forceinline__ float i8_silu_mul(uint32_t gi, uint32_t ui, float sa, float sg, float su) {
+  const float g = __int2float_rn(static_cast<int>(gi)) * (sa * sg);
+  const float u = __int2float_rn(static_cast<int>(ui)) * (sa * su);
+  return silu_mul(g, u);
+}
+
+// Eight consecutive outputs of EPI_I8_OUT at element `at`.
+__device__ __forceinline__ void i8_store8(const GemmArgs& args, int64_t at, const float (&v)[8]) {
+  if (args.out_f32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(args.out) + at);
+    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.out) + at) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                   pack_bf16x2(v[6], v[7]));
+  }
+}
+
 // Drain one accumulator (this warp's 32 TMEM lanes, BN columns starting at
 // t_row) and store the thread's row.  Every lane must call it (the TMEM loads
 // are warp-collective); row_ok masks only the stores.
@@ -261,6 +304,61 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs& args, int g, int r
               *reinterpret_cast<uint4*>(gu_row + col) = make_uint4(gp[0], gp[1], gp[2], gp[3]);
               *reinterpret_cast<uint4*>(gu_row + args.N + col) = make_uint4(up[0], up[1], up[2], up[3]);
             }
+          }
+        }
+      }
+    }
+  } else if constexpr (EPI == EPI_I8_SWIGLU) {
+    float* out_row = static_cast<float*>(args.out) + static_cast<int64_t>(row) * args.ldo +
+                     static_cast<int64_t>(g) * args.out_col_stride;
+    const float* bs = args.b_scale + g * args.b_scale_stride;
+    const float sa = row_ok ? args.a_scale[row] : 0.f;
+    unsigned amax = 0;
+#pragma unroll 1
+    for (int c = 0; c < BN / 2; c += 32) {
+      uint32_t gr[32], ur[32];
+      tmem_load_32x32(t_row + c, gr);
+      tmem_load_32x32(t_row + BN / 2 + c, ur);
+      tmem_load_wait();
+      if (row_ok) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int col = n0 + c + q * 4;
+          if (col < args.N) {
+            const float4 sg = *reinterpret_cast<const float4*>(bs + col);
+            const float4 su = *reinterpret_cast<const float4*>(bs + args.N + col);
+            const float h0 = i8_silu_mul(gr[q * 4], ur[q * 4], sa, sg.x, su.x);
+            const float h1 = i8_silu_mul(gr[q * 4 + 1], ur[q * 4 + 1], sa, sg.y, su.y);
+            const float h2 = i8_silu_mul(gr[q * 4 + 2], ur[q * 4 + 2], sa, sg.z, su.z);
+            const float h3 = i8_silu_mul(gr[q * 4 + 3], ur[q * 4 + 3], sa, sg.w, su.w);
+            amax = max(max(amax, max(abs_bits(h0), abs_bits(h1))), max(abs_bits(h2), abs_bits(h3)));
+            *reinterpret_cast<float4*>(out_row + col) = make_float4(h0, h1, h2, h3);
+          }
+        }
+      }
+    }
+    if (row_ok) atomicMax(args.row_amax + row, amax);
+  } else if constexpr (EPI == EPI_I8_OUT) {
+    const int64_t at = static_cast<int64_t>(row) * args.ldo + static_cast<int64_t>(g) * args.out_col_stride;
+    const float* bs = args.b_scale + g * args.b_scale_stride;
+    const float sa = row_ok ? args.a_scale[row] : 0.f;
+#pragma unroll 1
+    for (int c = 0; c < BN; c += 32) {
+      uint32_t vr[32];
+      tmem_load_32x32(t_row + c, vr);
+      tmem_load_wait();
+      if (row_ok) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int col = n0 + c + q * 8;
+          if (col < args.N) {
+            const float4 s0 = *reinterpret_cast<const float4*>(bs + col);
+            const float4 s1 = *reinterpret_cast<const float4*>(bs + col + 4);
+            const float sb[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __int2float_rn(static_cast<int>(vr[q * 8 + j])) * (sa * sb[j]);
+            i8_store8(args, at + col, v);
           }
         }
       }
@@ -430,10 +528,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           uint8_t* b_dst = sB + stage * C::kBBytes;
           mbar_arrive_expect_tx(&full[stage], C::kStageBytes);
           tma_load_2d(a_dst, mA, &full[stage], kg * A.K + kk, ti.row0);
-          if (EPI == EPI_SWIGLU) {
+          if (is_swiglu(EPI)) {
             tma_load_3d(b_dst, mB, &full[stage], kk, ti.n0, 2 * ti.w);
             tma_load_3d(b_dst + C::kBBytes / 2, mB, &full[stage], kk, ti.n0, 2 * ti.w + 1);
-          } else if (EPI == EPI_BF16) {
+          } else if (EPI != EPI_F32) {
             tma_load_3d(b_dst, mB, &full[stage], kk, ti.n0, ti.w * A.k_groups + kg);
           } else {
             tma_load_3d(b_dst, mB, &full[stage], kk, 0, 0);
@@ -455,7 +553,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(kBM, BN);
+      constexpr uint32_t idesc = is_i8(EPI) ? idesc_i8_s32(kBM, BN) : idesc_bf16_f32(kBM, BN);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = test_stall(drain, abort_flag, args.stall_ns);
@@ -482,8 +580,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint64_t adesc = smem_desc_k128(smem_addr(sA + stage * C::kABytes));
           const uint64_t bdesc = smem_desc_k128(smem_addr(sB + stage * C::kBBytes));
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)  // advance 16 elements = 32 bytes = 2 descriptor units
-            umma_bf16(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, (kb | k) != 0 ? 1u : 0u);
+          for (int k = 0; k < kBK / 16; ++k) {  // advance 16 elements = 32 bytes = 2 descriptor units
+            if constexpr (is_i8(EPI))
+              umma_i8(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, (kb | k) != 0 ? 1u : 0u);
+            else
+              umma_bf16(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, (kb | k) != 0 ? 1u : 0u);
+          }
           umma_commit(&empty[stage]);
           if (++stage == STAGES) {
             stage = 0;
@@ -601,8 +703,13 @@ __device__ __forceinline__ int pair_nkb(const GemmArgs& a, int kc) {
   return ((a.K + kBK * kc - 1) / (kBK * kc)) * a.k_groups;
 }
 
-// MMA N of a swap tile covering `rows` (1..256) token rows: a multiple of 16.
-__device__ __forceinline__ int swap_n(int rows) { return (rows + 15) & ~15; }
+// MMA N of a swap tile covering `rows` (1..256) token rows: a multiple of 16
+// (kind::i8 on a CTA pair: of 32).
+template <int EPI>
+__device__ __forceinline__ int swap_n(int rows) {
+  constexpr int kStep = is_i8(EPI) ? 32 : 16;
+  return (rows + kStep - 1) & ~(kStep - 1);
+}
 
 // Epilogue of a swap tile (all four epilogue warps, uniform control flow):
 // TMEM lane = weight row of this CTA, column = token of the tile.  Each
@@ -615,19 +722,68 @@ template <int EPI>
 __device__ __forceinline__ void epilogue_swap(const GemmArgs& args, const TileInfo& ti, uint32_t rank, int quarter,
                                               int lane, int et, uint32_t t_lane, float* xbuf) {
   const int rows = ti.row_end - ti.row0;
-  const int n = swap_n(rows);
+  const int n = swap_n<EPI>(rows);
   const int my_lane = quarter * 32 + lane;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(args.out) + static_cast<int64_t>(ti.row0) * args.ldo +
-                       static_cast<int64_t>(ti.g) * args.out_col_stride;
+  const int64_t out0 = static_cast<int64_t>(ti.row0) * args.ldo + static_cast<int64_t>(ti.g) * args.out_col_stride;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(args.out) + out0;
+  const float* bs = is_i8(EPI) ? args.b_scale + ti.g * args.b_scale_stride : nullptr;
 #pragma unroll 1
   for (int c = 0; c < n; c += 32) {
     uint32_t v[32];
     tmem_load_32x32(t_lane + c, v);
     tmem_load_wait();
 #pragma unroll
-    for (int j = 0; j < 32; ++j) xbuf[j * kSwapXStride + my_lane] = __uint_as_float(v[j]);
+    for (int j = 0; j < 32; ++j)
+      xbuf[j * kSwapXStride + my_lane] = is_i8(EPI) ? __int2float_rn(static_cast<int>(v[j])) : __uint_as_float(v[j]);
     named_bar_sync(1, 128);
-    if (EPI == EPI_SWIGLU) {
+    if constexpr (EPI == EPI_I8_SWIGLU) {
+      const int fg = et & 7;
+      const int f = ti.n0 + 64 * static_cast<int>(rank) + 8 * fg;
+#pragma unroll
+      for (int pass = 0; pass < 2; ++pass) {
+        const int j = pass * 16 + (et >> 3);
+        const bool ok = c + j < rows && f < args.N;
+        unsigned amax = 0;
+        if (ok) {
+          const float sa = args.a_scale[ti.row0 + c + j];
+          float* orow = static_cast<float*>(args.out) + out0 + static_cast<int64_t>(c + j) * args.ldo + f;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float4 g = *reinterpret_cast<const float4*>(xbuf + j * kSwapXStride + 8 * fg + 4 * q);
+            const float4 u = *reinterpret_cast<const float4*>(xbuf + j * kSwapXStride + 64 + 8 * fg + 4 * q);
+            const float4 sg = *reinterpret_cast<const float4*>(bs + f + 4 * q);
+            const float4 su = *reinterpret_cast<const float4*>(bs + args.N + f + 4 * q);
+            const float h0 = silu_mul(g.x * (sa * sg.x), u.x * (sa * su.x));
+            const float h1 = silu_mul(g.y * (sa * sg.y), u.y * (sa * su.y));
+            const float h2 = silu_mul(g.z * (sa * sg.z), u.z * (sa * su.z));
+            const float h3 = silu_mul(g.w * (sa * sg.w), u.w * (sa * su.w));
+            amax = max(max(amax, max(abs_bits(h0), abs_bits(h1))), max(abs_bits(h2), abs_bits(h3)));
+            *reinterpret_cast<float4*>(orow + 4 * q) = make_float4(h0, h1, h2, h3);
+          }
+        }
+        // the 8 lanes of one token hold 64 of its features: one atomic for them
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o, 8));
+        if (ok && fg == 0) atomicMax(args.row_amax + ti.row0 + c + j, amax);
+      }
+    } else if constexpr (EPI == EPI_I8_OUT) {
+      const int fg = et & 15;
+      const int col = ti.n0 + 128 * static_cast<int>(rank) + 8 * fg;
+#pragma unroll
+      for (int pass = 0; pass < 4; ++pass) {
+        const int j = pass * 8 + (et >> 4);
+        if (c + j < rows && col < args.N) {
+          const float sa = args.a_scale[ti.row0 + c + j];
+          const float4* vp = reinterpret_cast<const float4*>(xbuf + j * kSwapXStride + 8 * fg);
+          const float4 a = vp[0], b = vp[1];
+          const float4 s0 = *reinterpret_cast<const float4*>(bs + col);
+          const float4 s1 = *reinterpret_cast<const float4*>(bs + col + 4);
+          const float y[8] = {a.x * (sa * s0.x), a.y * (sa * s0.y), a.z * (sa * s0.z), a.w * (sa * s0.w),
+                              b.x * (sa * s1.x), b.y * (sa * s1.y), b.z * (sa * s1.z), b.w * (sa * s1.w)};
+          i8_store8(args, out0 + static_cast<int64_t>(c + j) * args.ldo + col, y);
+        }
+      }
+    } else if (EPI == EPI_SWIGLU) {
       // 64 features = 8 groups of 8: 16 tokens per pass
       const int fg = et & 7;
       const int f = ti.n0 + 64 * static_cast<int>(rank) + 8 * fg;
@@ -694,7 +850,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                              const __grid_constant__ CUtensorMap tmA32d, const __grid_constant__ CUtensorMap tmA16d,
                              const __grid_constant__ CUtensorMap tmB64d, const __grid_constant__ CUtensorMap tmA32d_2,
                              const __grid_constant__ CUtensorMap tmA16d_2, const __grid_constant__ CUtensorMap tmB64d_2) {
-  constexpr int kOutCols = (EPI == EPI_SWIGLU) ? kPairBN / 2 : kPairBN;
+  constexpr int kOutCols = is_swiglu(EPI) ? kPairBN / 2 : kPairBN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // stage s: smem + s * kPairStageBytes (tokens / A rows first, then weights)
@@ -793,7 +949,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const CUtensorMap* mB64 = ti.second ? &tmB64_2 : &tmB64;
         // a swap tile's N token rows are split N/2 per CTA; the box (16, 32,
         // 64 or 128 rows) may load more, the MMA reads the first N/2
-        const int half_n = ti.swap ? swap_n(ti.row_end - ti.row0) / 2 : 128;
+        const int half_n = ti.swap ? swap_n<EPI>(ti.row_end - ti.row0) / 2 : 128;
         const int a_box = ti.swap ? swap_box_rows(half_n) : 128;
         const int kc = pair_tile_kc(A, ti, a_box);
         const bool deep = kc == kDeepKC;
@@ -831,7 +987,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           }
           if (merge) {
             const CUtensorMap* wmap = deep ? (ti.second ? &tmB64d_2 : &tmB64d) : mB64;
-            if (EPI == EPI_SWIGLU)  // weights are the M operand: this CTA's 64 gate rows, then the same 64 up rows
+            if (is_swiglu(EPI))  // weights are the M operand: this CTA's 64 gate rows, then the same 64 up rows
               tma_load_4d_pair(b_dst, wmap, bar, 0, ti.n0 + 64 * static_cast<int>(rank), 2 * ti.w, kk0 / kBK);
             else
               tma_load_4d_pair(b_dst, wmap, bar, 0, ti.n0 + 128 * static_cast<int>(rank), ti.w * A.k_groups + kg,
@@ -841,11 +997,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             for (int c = 0; c < kPairKC; ++c) {
               const int kk = kk0 + c * kBK;
               uint8_t* bc = b_dst + c * kPairChunk;
-              if (EPI == EPI_SWIGLU && ti.swap) {
+              if (is_swiglu(EPI) && ti.swap) {
                 const int f = ti.n0 + 64 * static_cast<int>(rank);
                 tma_load_3d_pair(bc, mB64, bar, kk, f, 2 * ti.w);
                 tma_load_3d_pair(bc + kPairChunk / 2, mB64, bar, kk, f, 2 * ti.w + 1);
-              } else if (EPI == EPI_SWIGLU) {
+              } else if (is_swiglu(EPI)) {
                 tma_load_3d_pair(bc, mB, bar, kk, ti.n0, 2 * ti.w + static_cast<int>(rank));
               } else {
                 tma_load_3d_pair(bc, mB, bar, kk, ti.n0 + 128 * static_cast<int>(rank), ti.w * A.k_groups + kg);
@@ -881,13 +1037,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       int it = 0;
       for (int tile = pair; ok && tile < total_tiles; tile += n_pairs, ++it) {
         const TileInfo ti = decode_pair_tile(tile, tiles1, total_tiles, prefix, prefix2, args, args2, kOutCols);
-        const int a_box = ti.swap ? swap_box_rows(swap_n(ti.row_end - ti.row0) / 2) : 128;
+        const int a_box = ti.swap ? swap_box_rows(swap_n<EPI>(ti.row_end - ti.row0) / 2) : 128;
         const int kc = pair_tile_kc(ti.second ? args2 : args, ti, a_box);
         const int nkb = pair_nkb(ti.second ? args2 : args, kc);
         const int w_off = kc == kDeepKC ? kDeepWOffset : kPairABytes;
         // normal tile: A = token rows (M = 256), B = weight rows (N = 256);
         // swap tile: A = weight rows (M = 256), B = the tile's N token rows
-        const uint32_t idesc = idesc_bf16_f32(kPairBM, ti.swap ? swap_n(ti.row_end - ti.row0) : kPairBN);
+        const int mma_n = ti.swap ? swap_n<EPI>(ti.row_end - ti.row0) : kPairBN;
+        const uint32_t idesc = is_i8(EPI) ? idesc_i8_s32(kPairBM, mma_n) : idesc_bf16_f32(kPairBM, mma_n);
         // the token operand's chunks sit a_box rows apart (see the producer)
         const int a_chunk = a_box * kBK * 2;
         const int acc = it & 1;
@@ -913,8 +1070,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             const uint64_t adesc = ti.swap ? wdesc : tdesc;
             const uint64_t bdesc = ti.swap ? tdesc : wdesc;
 #pragma unroll
-            for (int k = 0; k < kBK / 16; ++k)
-              umma_bf16_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, (kb | c | k) != 0 ? 1u : 0u);
+            for (int k = 0; k < kBK / 16; ++k) {
+              if constexpr (is_i8(EPI))
+                umma_i8_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, (kb | c | k) != 0 ? 1u : 0u);
+              else
+                umma_bf16_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, (kb | c | k) != 0 ? 1u : 0u);
+            }
           }
           umma_commit_pair_multicast(&empty[stage], 0x3);
           if (++stage == kPairStages) {
@@ -1709,6 +1870,180 @@ int launch_expert_ffn_mixed(const Problem& p, const void* x_perm, const int32_t*
     return -3;
   r.a.clk = clk_down;
   return run_pair_gemm<EPI_BF16>(r, &s, st);
+}
+
+// ============================================================================
+// 8-bit products (kind::i8).  The maps view pairs of integers as 2-byte
+// elements, so every K below is half the number of integers.
+// ============================================================================
+// One group's problem on 128-row single-CTA tiles or 256-row CTA pairs.
+//   swiglu: w [G, 2N, K] (gate rows, then up rows), out FP32 rows + row_amax
+//   else:   w [G * k_groups, N, K], out BF16 or FP32
+struct I8Gemm {
+  const int8_t* a;      // [n_rows, k_groups * K]
+  const float* a_scale; // [n_rows]
+  int64_t n_rows;
+  const int32_t* seg_off;  // or nullptr: every group covers all rows
+  int n_groups;
+  const int8_t* w;
+  const float* w_scale;
+  int64_t w_scale_stride;
+  int N, K, k_groups;
+  void* out;
+  int64_t ldo;
+  int out_col_stride;
+  int out_f32;
+  unsigned* row_amax;
+  unsigned* status;
+};
+
+static void i8_args(const I8Gemm& q, GemmArgs* a) {
+  *a = GemmArgs{};
+  a->n_groups = q.n_groups;
+  a->seg_off = q.seg_off;
+  a->n_rows = static_cast<int>(q.n_rows);
+  a->N = q.N;
+  a->K = q.K / 2;
+  a->k_groups = q.k_groups;
+  a->out = q.out;
+  a->ldo = q.ldo;
+  a->out_col_stride = q.out_col_stride;
+  a->status = q.status;
+  a->a_scale = q.a_scale;
+  a->b_scale = q.w_scale;
+  a->b_scale_stride = q.w_scale_stride;
+  a->row_amax = q.row_amax;
+  a->out_f32 = q.out_f32;
+}
+
+static bool i8_pair_problem(const I8Gemm& g, bool swiglu, PairProblem* q) {
+  const int64_t K = g.K / 2;
+  const bool merged = merged_k_ok(K);
+  // B matrices: per group a gate and an up matrix, or k_groups matrices
+  const int64_t mats = static_cast<int64_t>(g.n_groups) * (swiglu ? 2 : g.k_groups);
+  const uint32_t swap_rows = swiglu ? 64 : 128, swap_mats = swiglu && merged ? 2 : 1;
+  if (!make_token_maps(&q->ta, &q->ta64, &q->ta32, &q->ta16, &q->ta32d, &q->ta16d, g.a, K * g.k_groups, g.n_rows,
+                       merged) ||
+      !make_weight_map(&q->tb, g.w, K, g.N, mats, 128, 1, false) ||
+      !make_weight_map(&q->tb64, g.w, K, g.N, mats, swap_rows, swap_mats, merged))
+    return false;
+  q->tb64d = q->tb64;
+  if (merged && !make_weight_map(&q->tb64d, g.w, K, g.N, mats, swap_rows, swap_mats, true, kDeepKC)) return false;
+  i8_args(g, &q->a);
+  q->a.swap_max = swap_max_rows();
+  q->a.merged_k = merged ? 1 : 0;
+  q->a.deep_swap = merged && deep_swap_on() ? 1 : 0;
+  const int64_t mt = g.seg_off ? cdiv(g.n_rows, kBM) + g.n_groups : g.n_groups * cdiv(g.n_rows, kBM);
+  q->tile_bound = (mt / 2 + g.n_groups) * cdiv(g.N, swiglu ? 128 : 256);
+  return true;
+}
+
+static bool i8_single_problem(const I8Gemm& g, bool swiglu, SingleProblem* q) {
+  const uint64_t K = static_cast<uint64_t>(g.K / 2);
+  const uint64_t da[2] = {K * g.k_groups, static_cast<uint64_t>(g.n_rows)};
+  const uint32_t ba[2] = {kBK, kBM};
+  const uint64_t db[3] = {K, static_cast<uint64_t>(g.N),
+                          static_cast<uint64_t>(g.n_groups) * (swiglu ? 2 : g.k_groups)};
+  const uint32_t bb[3] = {kBK, static_cast<uint32_t>(swiglu ? 128 : 256), 1};
+  if (!make_map(&q->ta, g.a, 2, da, ba) || !make_map(&q->tb, g.w, 3, db, bb)) return false;
+  i8_args(g, &q->a);
+  q->a.stall_ns = test_stall_ns();
+  const int64_t mt = g.seg_off ? cdiv(g.n_rows, kBM) + g.n_groups : g.n_groups * cdiv(g.n_rows, kBM);
+  q->tile_bound = mt * cdiv(g.N, swiglu ? 128 : 256);
+  return true;
+}
+
+// Tile shape by the rows a group is expected to hold, as the BF16 products.
+static bool i8_pairs(const I8Gemm& g) {
+  const int64_t expected = g.seg_off ? g.n_rows / g.n_groups : g.n_rows;
+  return tile_mode(expected) != kTileSingle;
+}
+
+template <int EPI>
+static int run_i8(const I8Gemm& g, cudaStream_t st) {
+  if (g.n_rows <= 0) return 0;
+  if (i8_pairs(g)) {
+    PairProblem q;
+    if (!i8_pair_problem(g, EPI == EPI_I8_SWIGLU, &q)) return -3;
+    return run_pair_gemm<EPI>(q, nullptr, st);
+  }
+  SingleProblem q;
+  if (!i8_single_problem(g, EPI == EPI_I8_SWIGLU, &q)) return -3;
+  return run_gemm<EPI, 256, 4>(q.ta, q.tb, q.a, q.tile_bound, st);
+}
+
+int launch_matmul_i8(const int8_t* x, const float* x_scale, int64_t n_rows, const int32_t* seg_off, int n_groups,
+                     const int8_t* w, const float* w_scale, int N, int K, int out_dtype, void* y, unsigned* status,
+                     cudaStream_t st) {
+  I8Gemm g{};
+  g.a = x;
+  g.a_scale = x_scale;
+  g.n_rows = n_rows;
+  g.seg_off = seg_off;
+  g.n_groups = n_groups;
+  g.w = w;
+  g.w_scale = w_scale;
+  g.w_scale_stride = N;
+  g.N = N;
+  g.K = K;
+  g.k_groups = 1;
+  g.out = y;
+  g.ldo = N;
+  g.out_f32 = out_dtype == kF32;
+  g.status = status;
+  return run_i8<EPI_I8_OUT>(g, st);
+}
+
+// The 8-bit expert FFN: up/gate product with SwiGLU, the hidden rows to 8
+// bits, down product.  Shared experts (mode 1): their hidden rows side by side
+// are one row of N_s F integers with one scale per token, and w2_scale [d] is
+// the scale of an output channel over all of them, so the down product sums
+// the N_s experts in the integer accumulator.
+int launch_expert_ffn_i8(const Problem& p, int mode, const int8_t* x, const float* x_scale, int64_t n_rows,
+                         const int32_t* seg_off, const int8_t* w13, const float* w13_scale, const int8_t* w2,
+                         const float* w2_scale, float* h, unsigned* amax, int8_t* hq, float* h_scale, void* y,
+                         unsigned* status, cudaStream_t st, bool amax_cleared) {
+  if (n_rows <= 0) return 0;
+  const bool routed = mode == 0;
+  const int h_cols = routed ? p.F : p.Ns * p.F;
+  if (!amax_cleared && cudaMemsetAsync(amax, 0, static_cast<size_t>(n_rows) * sizeof(unsigned), st) != cudaSuccess) return -3;
+  I8Gemm up{};
+  up.a = x;
+  up.a_scale = x_scale;
+  up.n_rows = n_rows;
+  up.seg_off = routed ? seg_off : nullptr;
+  up.n_groups = routed ? p.E : p.Ns;
+  up.w = w13;
+  up.w_scale = w13_scale;
+  up.w_scale_stride = 2 * static_cast<int64_t>(p.F);
+  up.N = p.F;
+  up.K = p.d;
+  up.k_groups = 1;
+  up.out = h;
+  up.ldo = h_cols;
+  up.out_col_stride = routed ? 0 : p.F;
+  up.row_amax = amax;
+  up.status = status;
+  if (int rc = run_i8<EPI_I8_SWIGLU>(up, st)) return rc;
+  if (launch_quantize_hidden(h, amax, routed ? seg_off + p.E : nullptr, n_rows, h_cols, hq, h_scale, st) !=
+      cudaSuccess)
+    return -3;
+  I8Gemm dn{};
+  dn.a = hq;
+  dn.a_scale = h_scale;
+  dn.n_rows = n_rows;
+  dn.seg_off = up.seg_off;
+  dn.n_groups = routed ? p.E : 1;
+  dn.w = w2;
+  dn.w_scale = w2_scale;
+  dn.w_scale_stride = p.d;
+  dn.N = p.d;
+  dn.K = p.F;
+  dn.k_groups = routed ? 1 : p.Ns;
+  dn.out = y;
+  dn.ldo = p.d;
+  dn.status = status;
+  return run_i8<EPI_I8_OUT>(dn, st);
 }
 
 }  // namespace moe

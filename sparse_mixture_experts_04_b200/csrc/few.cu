@@ -1,0 +1,1083 @@
+// The whole layer for a few tokens (1..64) in one kernel.
+//
+// With a handful of tokens the layer is a stream of weights: the experts that
+// got a row are read once, and everything else (routing, activations, the
+// combine) is small.  One cooperative kernel, one CTA per SM, keeps that stream
+// running from the first byte to the last instead of draining it at the ends
+// of six launches:
+//
+//   1. logits    tiles of 4 experts x 4 tokens over the CTAs        grid barrier
+//   2. routing   every CTA ranks all tokens itself (softmax, top-K, capacity,
+//                slots), so no barrier follows; CTA 0 writes the outputs
+//   3. up        h = silu(W_gate x) * (W_up x)                      grid barrier
+//   4. down      partial sums of W_down h, FP32                     grid barrier
+//   5. combine   y_t = sum of the shared experts + sum_k w_k Expert_k(x_t)
+//
+// Steps 3 and 4 are cut into units of 16 weight rows (8 gate rows and their 8
+// up rows; 16 output channels), whose reduction stays inside the CTA.  A CTA's
+// units are one contiguous range of the list (expert, reduction chunk, rows),
+// so a unit's tokens are usually in shared memory already.  The weights come
+// through a ring of shared-memory stages filled by bulk copies; the copies run
+// ahead of the arithmetic across units and across the grid barriers (weights
+// depend on no other CTA), so a barrier costs no bandwidth.
+//
+// Arithmetic: BF16 and 8-bit weights are the M operand of m16n8k16 / m16n8k32
+// tensor-core instructions (16 weight rows, 8 tokens), the 8 warps taking
+// 64-byte slices of the reduction in turn; the products of a unit are 16 x 8
+// numbers per warp, summed over the warps in shared memory in warp order.  The
+// tensor cores are nearly idle (a stage of 32 KB arrives in 1400 cycles and is
+// multiplied in some 250), which is why the simple warp-level instruction is
+// used and not tcgen05: its 128-row tiles would be 1..8 rows full.  FP32
+// weights take fused multiply-adds (8 rows x 8 tokens per lane).  No step
+// depends on the order in which CTAs run, so results repeat bit for bit.
+//
+// Every wait on the ring is bounded (mbar_wait); after a time-out the kernel
+// issues no more copies, waits for those in flight and reports
+// MOE_DEV_WAIT_TIMEOUT.  The grid barriers are cooperative groups' own: all
+// CTAs are resident (cooperative launch) and each reaches every barrier.
+#include <cooperative_groups.h>
+#include <math.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+#include "quant.cuh"
+#include "router_select.cuh"
+
+namespace moe {
+
+namespace cg = cooperative_groups;
+
+enum { kFewBF16 = 0, kFewF32 = 1, kFewI8 = 2 };
+
+constexpr int kFewWorkers = 256;                 // 8 warps
+constexpr int kFewThreads = kFewWorkers + 32;    // + one warp for the statistics
+constexpr int kFewRows = 16;                     // weight rows of a unit
+constexpr int kFewChunk = 2048;                  // bytes of each row in a stage
+constexpr int kFewPitch = kFewChunk + 16;        // odd number of 16-byte pieces: no bank conflicts
+constexpr int kFewStages = 4;
+constexpr int kFewStageBytes = kFewRows * kFewPitch;
+constexpr int kFewTokBytes = 69632;              // the unit's tokens (8 rows of 8 KB)
+constexpr int kFewMaxPairs = kFewMaxTokens * kMaxTopK;
+constexpr int kFewRedBytes = 2 * 8 * 2 * 128 * 4;  // [2][8 warps][2 token tiles][16 x 8] sums
+
+struct FewShared {
+  uint64_t full[kFewStages];
+  unsigned long long mask[kMaxExperts];   // tokens that chose the expert
+  unsigned long long psum[kMaxExperts];   // sum of p, fixed point; then f_e P_e as doubles (statistics)
+  double zsum[8];
+  int counts[kMaxExperts];
+  int kept[kMaxExperts];
+  int seg_off[kMaxExperts + 1];
+  int groups[kMaxExperts + 1];            // prefix of the experts' token groups
+  uint16_t perm[kFewMaxPairs];            // slot -> t * K + k
+  float row_scale[16];                    // 8-bit tokens: scale of each row in the token buffer
+  int abort_flag;
+};
+
+constexpr int few_smem_bytes() {
+  return kFewStages * kFewStageBytes + kFewTokBytes + kFewRedBytes + static_cast<int>(sizeof(FewShared)) + 128;
+}
+static_assert(few_smem_bytes() <= 227 * 1024, "shared memory of the few-token kernel");
+
+struct FewArgs {
+  const void* x;
+  const void* w_gate;
+  const float* logit_offset;
+  const float* sel_bias;
+  const int32_t* expert_cap;  // per-expert capacities, or nullptr
+  const char* w13;
+  const char* w2;
+  const char* w13_s;
+  const char* w2_s;
+  const float* s13;    // 8-bit weights: scales [E, 2F], [E, d], [N_s, 2F], [d]
+  const float* s2;
+  const float* s13_s;
+  const float* s2_s;
+  void* y;
+  float* logits;
+  int32_t* topk_idx;
+  float* topk_w;
+  int32_t* counts;
+  int32_t* kept;
+  int32_t* seg_off;
+  int32_t* slot_of;
+  int32_t* perm;
+  float* stats;        // or nullptr
+  void* h;             // [T K, F] hidden rows by slot: BF16, or FP32 (FP32 and 8-bit weights)
+  void* h_s;           // [T, N_s F]
+  unsigned* amax;      // 8-bit: bits of max|h| by slot, then by token for the shared experts
+  float* part;         // [nc][T K][d] partial sums by slot
+  float* part_s;       // [N_s nc][T][d]
+  unsigned* status;
+  int T, d, E, K, Ns, F;
+  long long cap;       // -1: no limit
+  int given, bias_on_logit, extended;
+  float alpha;
+  double pscale;
+  // tiling (host): token rows per group, reduction chunks of the down product
+  int ng_up, ng_down, nc, chunk_bytes;
+};
+
+// ------------------------------------------------------------ small helpers
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t saddr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+
+__device__ __forceinline__ void mma_16x8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_16x8(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
+
+// The four passes over weights: shared and routed experts, up and down.
+enum { kUpShared = 0, kUpRouted = 1, kDownShared = 2, kDownRouted = 3, kPasses = 4 };
+
+// Where the units of one pass lie and which of them are this CTA's.
+struct PassRange {
+  int first, last;  // units [first, last)
+};
+
+// A unit, decoded: which weights, which tokens.
+struct Unit {
+  const char* w;       // row 0 of the unit at the start of its reduction
+  int64_t hi;          // byte offset from row r < 8 to row r + 8
+  int64_t row_bytes;   // distance between rows
+  int rows;            // valid rows: 16, or 8 at the end of d
+  int len;             // bytes of each row in the unit's reduction
+  int e;               // expert (routed or shared)
+  int row0, n;         // first token row (slot or token) and their number
+  int c;               // reduction chunk (down)
+  int col;             // first feature / output channel
+};
+
+template <int WT>
+struct Few {
+  static constexpr int kW = WT == kFewF32 ? 4 : WT == kFewBF16 ? 2 : 1;  // bytes of a weight
+  static constexpr int kTiles = WT == kFewF32 ? 1 : 2;                   // 8-token tiles of a group
+  using Acc = typename std::conditional<WT == kFewI8, int, float>::type;
+
+  const FewArgs& a;
+  FewShared& s;
+  uint8_t* ring;
+  uint8_t* tok;
+  int cta, n_cta, nfb, nb;
+
+  __device__ __forceinline__ Few(const FewArgs& a_, FewShared& s_, uint8_t* ring_, uint8_t* tok_)
+      : a(a_), s(s_), ring(ring_), tok(tok_), cta(blockIdx.x), n_cta(gridDim.x), nfb(a_.F / 8),
+        nb((a_.d + kFewRows - 1) / kFewRows) {}
+
+  // token groups of the shared experts / of the routed ones, for rows per group ng
+  __device__ __forceinline__ int shared_groups(int ng) const { return (a.T + ng - 1) / ng; }
+
+  // units of a pass (routed passes: s.groups is the up or the down prefix)
+  __device__ __forceinline__ int64_t units(int pass) const {
+    if (pass == kUpShared) return static_cast<int64_t>(a.Ns) * shared_groups(a.ng_up) * nfb;
+    if (pass == kUpRouted) return static_cast<int64_t>(s.groups[a.E]) * nfb;
+    if (pass == kDownShared) return static_cast<int64_t>(a.Ns) * a.nc * shared_groups(a.ng_down) * nb;
+    return static_cast<int64_t>(s.groups[a.E]) * a.nc * nb;
+  }
+  __device__ __forceinline__ PassRange range(int pass) const {
+    const int64_t n = units(pass);
+    return PassRange{static_cast<int>(n * cta / n_cta), static_cast<int>(n * (cta + 1) / n_cta)};
+  }
+
+  // expert of routed token group v (largest e with groups[e] <= v that has groups)
+  __device__ __forceinline__ int group_expert(int v) const {
+    int lo = 0, hi = a.E - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.groups[mid] <= v) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  }
+
+  __device__ __forceinline__ Unit unit(int pass, int u) const {
+    Unit q;
+    const bool up = pass <= kUpRouted;
+    const int ng = up ? a.ng_up : a.ng_down;
+    int v, blk;
+    if (up) {
+      v = u / nfb;
+      blk = u - v * nfb;
+      q.c = 0;
+    } else {
+      const int t = u / nb;
+      blk = u - t * nb;
+      v = t / a.nc;
+      q.c = t - v * a.nc;
+    }
+    const char* base;
+    if (pass == kUpShared || pass == kDownShared) {
+      const int sg = shared_groups(ng);
+      q.e = v / sg;
+      q.row0 = (v - q.e * sg) * ng;
+      q.n = min(ng, a.T - q.row0);
+      base = up ? a.w13_s : a.w2_s;
+    } else {
+      q.e = group_expert(v);
+      q.row0 = s.seg_off[q.e] + (v - s.groups[q.e]) * ng;
+      q.n = min(ng, s.seg_off[q.e + 1] - q.row0);
+      base = up ? a.w13 : a.w2;
+    }
+    if (up) {
+      q.row_bytes = static_cast<int64_t>(a.d) * kW;
+      q.col = blk * 8;
+      q.rows = 16;
+      q.len = a.d * kW;
+      q.hi = a.F * q.row_bytes;
+      q.w = base + (static_cast<int64_t>(q.e) * 2 * a.F + q.col) * q.row_bytes;
+    } else {
+      q.row_bytes = static_cast<int64_t>(a.F) * kW;
+      q.col = blk * kFewRows;
+      q.rows = min(kFewRows, a.d - q.col);
+      const int64_t k0 = static_cast<int64_t>(q.c) * a.chunk_bytes;
+      q.len = static_cast<int>(min(static_cast<int64_t>(a.chunk_bytes), q.row_bytes - k0));
+      q.hi = 8 * q.row_bytes;
+      q.w = base + (static_cast<int64_t>(q.e) * a.d + q.col) * q.row_bytes + k0;
+    }
+    return q;
+  }
+};
+
+// The copy side of the ring: the next stage to fill, walked in the order in
+// which the stages are consumed.  Kept by every lane of warp 0 alike.
+struct Cursor {
+  int pass = 0, u = 0, end = 0, off = 0;
+  bool loaded = false;   // cur holds unit u
+  uint32_t issued = 0;   // stages filled so far
+  Unit cur;
+};
+
+// Fill the next stage (warp 0).  last_pass: the last pass whose units are
+// known.  Returns false when there is nothing (yet) to copy.
+template <int WT>
+__device__ __forceinline__ bool few_issue(const Few<WT>& f, Cursor& c, int last_pass, int lane) {
+  while (c.u >= c.end) {
+    if (c.pass >= last_pass) return false;
+    ++c.pass;
+    const PassRange r = f.range(c.pass);
+    c.u = r.first;
+    c.end = r.last;
+    c.loaded = false;
+    c.off = 0;
+  }
+  // one lane's reading decides for the warp
+  if (__shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&f.s.abort_flag), 0)) return false;
+  if (!c.loaded) {
+    c.cur = f.unit(c.pass, c.u);
+    c.loaded = true;
+  }
+  const int slot = static_cast<int>(c.issued % kFewStages);
+  const int bytes = min(kFewChunk, c.cur.len - c.off);
+  uint64_t* bar = &f.s.full[slot];
+  if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(c.cur.rows * bytes));
+  __syncwarp();
+  if (lane < c.cur.rows) {
+    const char* src = c.cur.w + (lane & 7) * c.cur.row_bytes + (lane >> 3) * c.cur.hi + c.off;
+    bulk_load(f.ring + slot * kFewStageBytes + lane * kFewPitch, src, static_cast<uint32_t>(bytes), bar);
+  }
+  ++c.issued;
+  c.off += bytes;
+  if (c.off >= c.cur.len) {
+    ++c.u;
+    c.loaded = false;
+    c.off = 0;
+  }
+  return true;
+}
+
+// One stage's products (cb bytes of each row): acc += weights x tokens.
+template <int WT>
+struct FewMath;
+
+template <int WT>
+struct FewMathMma {
+  using Acc = typename Few<WT>::Acc;
+  Acc acc[2][4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0;
+  }
+  // w: the stage; t: the token buffer at the stage's first byte of the rows
+  __device__ __forceinline__ void stage(const uint8_t* w, const uint8_t* t, int t_pitch, int cb, int n_tok, int rows,
+                                        int warp, int lane) {
+    // ldmatrix lane addresses: weights as four 8 x 16-byte blocks (rows 0-7 and
+    // 8-15, bytes 0-15 and 16-31); tokens as 8 rows x 64 bytes
+    const uint32_t wa = smem_addr(w) + (lane & 15) * kFewPitch + (lane >> 4) * 16;
+    // (rows past the group's last repeat it: their sums are not read)
+    const uint32_t ta = smem_addr(t) + min(lane & 7, n_tok - 1) * t_pitch + (lane >> 3) * 16;
+    const uint32_t tb = smem_addr(t) + min(8 + (lane & 7), n_tok - 1) * t_pitch + (lane >> 3) * 16;
+    for (int o = warp * 64; o < cb; o += 8 * 64) {
+      uint32_t a0[4], a1[4], b[4];
+      ldmatrix_x4(wa + o, a0);
+      ldmatrix_x4(wa + o + 32, a1);
+      if (o + 64 > cb) {  // the row ends inside: what lies behind it may be anything
+        if (o + 16 >= cb) a0[2] = a0[3] = 0;
+        if (o + 32 >= cb) a1[0] = a1[1] = 0;
+        if (o + 48 >= cb) a1[2] = a1[3] = 0;
+      }
+      if (rows == 8) a0[1] = a0[3] = a1[1] = a1[3] = 0;
+      ldmatrix_x4(ta + o, b);
+      mma_16x8(acc[0], a0, b[0], b[1]);
+      mma_16x8(acc[0], a1, b[2], b[3]);
+      if (n_tok > 8) {
+        ldmatrix_x4(tb + o, b);
+        mma_16x8(acc[1], a0, b[0], b[1]);
+        mma_16x8(acc[1], a1, b[2], b[3]);
+      }
+    }
+  }
+  // this warp's sums to red[warp][tile][row][token]
+  __device__ __forceinline__ void put(void* red, int n_tok, int warp, int lane) {
+    Acc* r = static_cast<Acc*>(red) + warp * 256 + (lane >> 2) * 8 + (lane & 3) * 2;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (j * 8 >= n_tok) break;
+      r[j * 128] = acc[j][0];
+      r[j * 128 + 1] = acc[j][1];
+      r[j * 128 + 64] = acc[j][2];
+      r[j * 128 + 65] = acc[j][3];
+    }
+  }
+  __device__ __forceinline__ static Acc get(const void* red, int row, int tok) {
+    const Acc* r = static_cast<const Acc*>(red) + (tok >> 3) * 128 + row * 8 + (tok & 7);
+    Acc v = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += r[w * 256];
+    return v;
+  }
+};
+
+template <>
+struct FewMath<kFewBF16> : FewMathMma<kFewBF16> {};
+template <>
+struct FewMath<kFewI8> : FewMathMma<kFewI8> {};
+
+// FP32: warp w takes rows (w >> 2) * 8 .. + 7 and the 512-byte slice w & 3 of a
+// stage, a lane 16 bytes of it.
+template <>
+struct FewMath<kFewF32> {
+  using Acc = float;
+  float acc[8][8];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[r][j] = 0.f;
+  }
+  __device__ __forceinline__ void stage(const uint8_t* w, const uint8_t* t, int t_pitch, int cb, int n_tok, int rows,
+                                        int warp, int lane) {
+    const int o = (warp & 3) * 512 + lane * 16;
+    if (o >= cb || (warp >> 2) * 8 >= rows) return;
+    const uint8_t* wr = w + (warp >> 2) * 8 * kFewPitch + o;
+    float4 wv[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) wv[r] = *reinterpret_cast<const float4*>(wr + r * kFewPitch);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j < n_tok) {
+        const float4 tv = *reinterpret_cast<const float4*>(t + j * t_pitch + o);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          acc[r][j] = fmaf(wv[r].x, tv.x, acc[r][j]);
+          acc[r][j] = fmaf(wv[r].y, tv.y, acc[r][j]);
+          acc[r][j] = fmaf(wv[r].z, tv.z, acc[r][j]);
+          acc[r][j] = fmaf(wv[r].w, tv.w, acc[r][j]);
+        }
+      }
+    }
+  }
+  // sum over the lanes by halving: lane l ends with entries 2l and 2l + 1 of [8 rows][8 tokens]
+  __device__ __forceinline__ void put(void* red, int, int warp, int lane) {
+    float v[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] = acc[i >> 3][i & 7];
+#pragma unroll
+    for (int o = 16, m = 32; o > 0; o >>= 1, m >>= 1) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (i < m) {
+          const float send = (lane & o) ? v[i] : v[i + m];
+          const float keep = (lane & o) ? v[i + m] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+      }
+    }
+    *reinterpret_cast<float2*>(static_cast<float*>(red) + warp * 64 + 2 * lane) = make_float2(v[0], v[1]);
+  }
+  __device__ __forceinline__ static float get(const void* red, int row, int tok) {
+    const float* r = static_cast<const float*>(red) + (row >> 3) * 4 * 64 + (row & 7) * 8 + tok;
+    return (r[0] + r[64]) + (r[128] + r[192]);
+  }
+};
+
+// ---------------------------------------------------------------- token rows
+// Rows of the unit's group into the token buffer, zero behind the row's end up
+// to the next multiple of 64 bytes.  up: rows of x; down: a chunk of hidden rows.
+template <int WT>
+__device__ __forceinline__ void few_load_tokens(const Few<WT>& f, int pass, const Unit& q, int t_pitch, int tid) {
+  const FewArgs& a = f.a;
+  const bool up = pass <= kUpRouted;
+  const bool routed = pass == kUpRouted || pass == kDownRouted;
+  const int pad = ((q.len + 63) & ~63) - q.len;
+  if constexpr (WT != kFewI8) {
+    const int vecs = q.len / 16, all = vecs + pad / 16;
+    for (int i = tid; i < q.n * all; i += kFewWorkers) {
+      const int r = i / all, v = i - r * all;
+      const char* src;
+      if (up) {
+        const int t = routed ? f.s.perm[q.row0 + r] / a.K : q.row0 + r;
+        src = static_cast<const char*>(a.x) + static_cast<int64_t>(t) * q.len;
+      } else if (routed) {
+        src = static_cast<const char*>(a.h) + (static_cast<int64_t>(q.row0 + r) * a.F) * Few<WT>::kW +
+              static_cast<int64_t>(q.c) * a.chunk_bytes;
+      } else {
+        src = static_cast<const char*>(a.h_s) +
+              (static_cast<int64_t>(q.row0 + r) * a.Ns + q.e) * a.F * Few<WT>::kW +
+              static_cast<int64_t>(q.c) * a.chunk_bytes;
+      }
+      const uint4 z = v < vecs ? __ldcg(reinterpret_cast<const uint4*>(src) + v) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(f.tok + r * t_pitch + v * 16) = z;
+    }
+  } else {
+    const int warp = tid >> 5, lane = tid & 31;
+    for (int r = warp; r < q.n; r += kFewWorkers / 32) {
+      uint8_t* dst = f.tok + r * t_pitch;
+      float scale;
+      if (up) {  // BF16 token row: its largest magnitude, then the integers
+        const int t = routed ? f.s.perm[q.row0 + r] / a.K : q.row0 + r;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) +
+                                                          static_cast<int64_t>(t) * a.d);
+        unsigned m = 0;
+        for (int v = lane; v < a.d / 8; v += 32) {
+          const uint4 w = src[v];
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m = max(m, max((u[i] << 16) & 0x7FFF0000u, u[i] & 0x7FFF0000u));
+        }
+        scale = quant_scale(warp_max_u32(m));
+        const float inv = 1.0f / scale;
+        for (int v = lane; v < a.d / 8; v += 32) {
+          const uint4 w = src[v];
+          const float lo[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+          const float hi[4] = {bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
+          *reinterpret_cast<uint2*>(dst + v * 8) =
+              make_uint2(quant_pack4(lo, scale, inv), quant_pack4(hi, scale, inv));
+        }
+      } else {  // FP32 hidden row whose largest magnitude every CTA has contributed to
+        const int64_t row = q.row0 + r;
+        const float* src = (routed ? static_cast<const float*>(a.h) + row * a.F
+                                   : static_cast<const float*>(a.h_s) + (row * a.Ns + q.e) * a.F) +
+                           static_cast<int64_t>(q.c) * a.chunk_bytes;
+        scale = quant_scale(__ldcg(a.amax + (routed ? row : static_cast<int64_t>(a.T) * a.K + row)));
+        const float inv = 1.0f / scale;
+        for (int v = lane; v < q.len / 4; v += 32) {
+          const float4 w = __ldcg(reinterpret_cast<const float4*>(src) + v);
+          const float z[4] = {w.x, w.y, w.z, w.w};
+          *reinterpret_cast<uint32_t*>(dst + v * 4) = quant_pack4(z, scale, inv);
+        }
+      }
+      if (lane < pad / 16) *reinterpret_cast<uint4*>(dst + q.len + lane * 16) = make_uint4(0, 0, 0, 0);
+      if (lane == 0) f.s.row_scale[r] = scale;
+    }
+  }
+}
+
+// ------------------------------------------------------------- unit outputs
+template <int WT>
+__device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const Unit& q, const void* red, int tid) {
+  using M = FewMath<WT>;
+  const FewArgs& a = f.a;
+  if (pass <= kUpRouted) {  // 8 features x n tokens: lane groups of 8 share a token
+    const int ft = tid & 7, tok = tid >> 3;
+    const bool live = tok < q.n;
+    float h = 0.f;
+    if (live) {
+      if constexpr (WT == kFewI8) {
+        const float* sc = (pass == kUpShared ? a.s13_s : a.s13) + static_cast<int64_t>(q.e) * 2 * a.F + q.col + ft;
+        const float sx = f.s.row_scale[tok];
+        const float g = __int2float_rn(M::get(red, ft, tok)) * (sx * sc[0]);
+        const float u = __int2float_rn(M::get(red, ft + 8, tok)) * (sx * sc[a.F]);
+        h = silu(g) * u;
+      } else {
+        h = silu(M::get(red, ft, tok)) * M::get(red, ft + 8, tok);
+      }
+      const int64_t row = q.row0 + tok;
+      const int64_t at = pass == kUpShared ? (row * a.Ns + q.e) * a.F + q.col + ft : row * a.F + q.col + ft;
+      void* hp = pass == kUpShared ? a.h_s : a.h;
+      if constexpr (WT == kFewBF16)
+        static_cast<__nv_bfloat16*>(hp)[at] = __float2bfloat16(h);
+      else
+        static_cast<float*>(hp)[at] = h;
+    }
+    if constexpr (WT == kFewI8) {
+      unsigned m = abs_bits(h);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o, 8));
+      if (live && ft == 0)
+        atomicMax(a.amax + (pass == kUpShared ? static_cast<int64_t>(a.T) * a.K : 0) + q.row0 + tok, m);
+    }
+  } else {  // 16 output channels x n tokens
+    const int n = tid & 15, tok = tid >> 4;
+    if (tok < q.n && n < q.rows) {
+      float v;
+      if constexpr (WT == kFewI8) {
+        const float sw = pass == kDownShared ? a.s2_s[q.col + n] : a.s2[static_cast<int64_t>(q.e) * a.d + q.col + n];
+        v = __int2float_rn(M::get(red, n, tok)) * (f.s.row_scale[tok] * sw);
+      } else {
+        v = M::get(red, n, tok);
+      }
+      const int64_t row = q.row0 + tok;
+      if (pass == kDownShared)
+        a.part_s[((static_cast<int64_t>(q.e) * a.nc + q.c) * a.T + row) * a.d + q.col + n] = v;
+      else
+        a.part[(static_cast<int64_t>(q.c) * a.T * a.K + row) * a.d + q.col + n] = v;
+    }
+  }
+}
+
+// All units of one pass that are this CTA's (the 256 worker threads).
+template <int WT>
+__device__ __forceinline__ void few_pass(const Few<WT>& f, int pass, Cursor& cur, uint32_t& used, uint8_t* red_base,
+                                         uint32_t& n_units, int last_pass, int tid) {
+  const int warp = tid >> 5, lane = tid & 31;
+  const PassRange r = f.range(pass);
+  FewMath<WT> math;
+  int held_e = -1, held_row = -1, held_c = -1;
+  for (int u = r.first; u < r.last; ++u) {
+    const Unit q = f.unit(pass, u);
+    const int t_pitch = ((q.len + 63) & ~63) + 16;
+    if (q.e != held_e || q.row0 != held_row || q.c != held_c) {
+      // the last unit's reads of the buffer (and of the row scales) are over
+      // only once its outputs are stored
+      named_bar_sync(1, kFewWorkers);
+      few_load_tokens(f, pass, q, t_pitch, tid);
+      held_e = q.e;
+      held_row = q.row0;
+      held_c = q.c;
+      named_bar_sync(1, kFewWorkers);
+    }
+    math.clear();
+    uint8_t* red = red_base + (n_units & 1u) * (kFewRedBytes / 2);
+    for (int off = 0; off < q.len; off += kFewChunk) {
+      const int slot = static_cast<int>(used % kFewStages);
+      mbar_wait(&f.s.full[slot], (used / kFewStages) & 1u, &f.s.abort_flag);
+      __syncwarp();
+      math.stage(f.ring + slot * kFewStageBytes, f.tok + off, t_pitch, min(kFewChunk, q.len - off), q.n, q.rows, warp,
+                 lane);
+      if (off + kFewChunk >= q.len) math.put(red, q.n, warp, lane);
+      ++used;
+      named_bar_sync(1, kFewWorkers);  // the stage is free, the sums are complete
+      if (warp == 0) few_issue(f, cur, last_pass, lane);
+    }
+    few_store_unit(f, pass, q, red, tid);
+    ++n_units;  // the next unit's sums go to the other half: no barrier before they are written
+  }
+}
+
+// ------------------------------------------------------------------- routing
+// Tiles of 4 experts x 4 tokens: the 8 warps split d, a lane takes 16 bytes of
+// each row per step, products are summed in FP32 per lane, the lanes and warps
+// in FP64.
+template <typename T>
+__device__ __forceinline__ void few_logits(const FewArgs& a, double* red, int tid) {
+  constexpr int V = 16 / static_cast<int>(sizeof(T));
+  const int warp = tid >> 5, lane = tid & 31;
+  const int te = (a.E + 3) / 4, tt = (a.T + 3) / 4;
+  for (int tile = blockIdx.x; tile < te * tt; tile += gridDim.x) {
+    const int e0 = (tile % te) * 4, t0 = (tile / te) * 4;
+    float acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i >> 2][i & 3] = 0.f;
+    for (int k = (warp * 32 + lane) * V; k < a.d; k += kFewWorkers * V) {
+      float w[4][V], x[4][V];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // rows past the end repeat the last one; their sums are not stored
+        const uint4 qw = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.w_gate) +
+                                                         static_cast<int64_t>(min(e0 + i, a.E - 1)) * a.d + k);
+        const uint4 qx = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) +
+                                                         static_cast<int64_t>(min(t0 + i, a.T - 1)) * a.d + k);
+        if constexpr (sizeof(T) == 2) {
+          unpack16(qw, w[i], static_cast<const __nv_bfloat16*>(nullptr));
+          unpack16(qx, x[i], static_cast<const __nv_bfloat16*>(nullptr));
+        } else {
+          w[i][0] = __uint_as_float(qw.x); w[i][1] = __uint_as_float(qw.y);
+          w[i][2] = __uint_as_float(qw.z); w[i][3] = __uint_as_float(qw.w);
+          x[i][0] = __uint_as_float(qx.x); x[i][1] = __uint_as_float(qx.y);
+          x[i][2] = __uint_as_float(qx.z); x[i][3] = __uint_as_float(qx.w);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[i][j] = fmaf(w[i][v], x[j][v], acc[i][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const double s = warp_sum(static_cast<double>(acc[i >> 2][i & 3]));
+      if (lane == 0) red[warp * 16 + i] = s;
+    }
+    named_bar_sync(1, kFewWorkers);
+    if (tid < 16) {
+      const int e = e0 + (tid >> 2), t = t0 + (tid & 3);
+      if (e < a.E && t < a.T) {
+        double s = 0.0;
+        for (int w = 0; w < 8; ++w) s += red[w * 16 + tid];
+        a.logits[static_cast<int64_t>(t) * a.E + e] =
+            static_cast<float>(s + (a.logit_offset ? static_cast<double>(a.logit_offset[e]) : 0.0));
+      }
+    }
+    named_bar_sync(1, kFewWorkers);
+  }
+}
+
+// Softmax and top-K of every token (each warp its own), into idx / w [T K].
+template <int EPL>
+__device__ __forceinline__ void few_select(const FewArgs& a, FewShared& s, int32_t* idx, float* w, bool with_stats,
+                                           int tid) {
+  const int warp = tid >> 5, lane = tid & 31;
+  float bias[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + 32 * i;
+    bias[i] = (a.sel_bias && e < a.E) ? a.sel_bias[e] : 0.f;
+  }
+  float zacc = 0.f;
+  double zsum = 0.0;
+  for (int t = warp; t < a.T; t += kFewWorkers / 32) {
+    float lg[EPL], p[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane + 32 * i;
+      lg[i] = e < a.E ? __ldcg(a.logits + static_cast<int64_t>(t) * a.E + e) : -INFINITY;
+      p[i] = 0.f;
+    }
+    zacc = 0.f;
+    select_token_group<EPL, 32>(lg, bias, a.sel_bias != nullptr, a.bias_on_logit, a.E, a.K, lane, p, zacc,
+                                idx + t * a.K, w + t * a.K, s.counts);
+    zsum += static_cast<double>(zacc);
+    if (with_stats) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (lane + 32 * i < a.E && p[i] > 0.f)
+          atomicAdd(&s.psum[lane + 32 * i], __double2ull_rn(static_cast<double>(p[i]) * a.pscale));
+    }
+  }
+  if (lane == 0) s.zsum[warp] = zsum;
+}
+
+// Capacity, slots and the experts' token groups from idx (the 256 workers).
+__device__ __forceinline__ void few_dispatch(const FewArgs& a, FewShared& s, const int32_t* idx, const float* w,
+                                             bool write, int tid) {
+  const int TK = a.T * a.K;
+  for (int i = tid; i < TK; i += kFewWorkers) {
+    const int e = idx[i];
+    if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicOr(&s.mask[e], 1ull << (i / a.K));
+  }
+  named_bar_sync(1, kFewWorkers);
+  if (tid < a.E) {
+    const int n = __popcll(s.mask[tid]);
+    long long cap = a.cap;
+    if (a.expert_cap) cap = a.expert_cap[tid];
+    const int k = (cap < 0 || n < cap) ? n : static_cast<int>(cap);
+    s.kept[tid] = k;
+    if (write) {
+      a.counts[tid] = n;
+      a.kept[tid] = k;
+    }
+  }
+  named_bar_sync(1, kFewWorkers);
+  if (tid < 32) {  // exclusive prefix over the experts, 8 per lane
+    int k[kMaxExperts / 32], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i) {
+      const int e = tid * (kMaxExperts / 32) + i;
+      k[i] = e < a.E ? s.kept[e] : 0;
+      sum += k[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (tid >= o) incl += v;
+    }
+    int run = incl - sum;
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i) {
+      const int e = tid * (kMaxExperts / 32) + i;
+      if (e <= a.E) {
+        s.seg_off[e] = run;
+        if (write) a.seg_off[e] = run;
+      }
+      run += k[i];
+    }
+    if (tid == 31 && a.E == kMaxExperts) {
+      s.seg_off[kMaxExperts] = run;
+      if (write) a.seg_off[kMaxExperts] = run;
+    }
+  }
+  named_bar_sync(1, kFewWorkers);
+  for (int i = tid; i < TK; i += kFewWorkers) {
+    const int e = idx[i], t = i / a.K;
+    int slot = -1;
+    if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) {
+      const int rank = __popcll(s.mask[e] & ((1ull << t) - 1ull));  // earlier tokens of the same expert
+      if (rank < s.kept[e]) slot = s.seg_off[e] + rank;
+    }
+    if (slot >= 0) s.perm[slot] = static_cast<uint16_t>(i);
+    if (write) {
+      a.topk_idx[i] = e;
+      a.topk_w[i] = w[i];
+      a.slot_of[i] = slot;
+      if (slot >= 0) a.perm[slot] = i;
+    }
+  }
+}
+
+// s.groups: prefix of ceil(kept / ng) over the experts (one warp)
+__device__ __forceinline__ void few_groups(const FewArgs& a, FewShared& s, int ng, int lane) {
+  int g[kMaxExperts / 32], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxExperts / 32; ++i) {
+    const int e = lane * (kMaxExperts / 32) + i;
+    g[i] = e < a.E ? (s.kept[e] + ng - 1) / ng : 0;
+    sum += g[i];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  int run = incl - sum;
+#pragma unroll
+  for (int i = 0; i < kMaxExperts / 32; ++i) {
+    const int e = lane * (kMaxExperts / 32) + i;
+    if (e <= a.E) s.groups[e] = run;
+    run += g[i];
+  }
+  if (lane == 31 && a.E == kMaxExperts) s.groups[kMaxExperts] = run;
+}
+
+// y_t = sum over the shared experts' chunks + sum_k w_k (sum of Expert_k's chunks)
+template <typename T>
+__device__ __forceinline__ void few_combine(const FewArgs& a, int tid) {
+  const int vecs = a.d / 4;
+  const int64_t total = static_cast<int64_t>(a.T) * vecs;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kFewWorkers + tid; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kFewWorkers) {
+    const int t = static_cast<int>(i / vecs), c = static_cast<int>(i - static_cast<int64_t>(t) * vecs) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int n = 0; n < a.Ns * a.nc; ++n) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_s + (static_cast<int64_t>(n) * a.T + t) * a.d + c));
+      acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    }
+    for (int k = 0; k < a.K; ++k) {
+      const int slot = __ldcg(a.slot_of + t * a.K + k);
+      if (slot < 0) continue;
+      const float w = __ldcg(a.topk_w + t * a.K + k);
+      float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int n = 0; n < a.nc; ++n) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(
+            a.part + (static_cast<int64_t>(n) * a.T * a.K + slot) * a.d + c));
+        e.x += v.x; e.y += v.y; e.z += v.z; e.w += v.w;
+      }
+      acc.x = fmaf(w, e.x, acc.x); acc.y = fmaf(w, e.y, acc.y);
+      acc.z = fmaf(w, e.z, acc.z); acc.w = fmaf(w, e.w, acc.w);
+    }
+    T* yp = static_cast<T*>(a.y) + static_cast<int64_t>(t) * a.d + c;
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(yp) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    else
+      *reinterpret_cast<float4*>(yp) = acc;
+  }
+}
+
+template <int WT>
+__global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_constant__ FewArgs a) {
+  using X = typename std::conditional<WT == kFewF32, float, __nv_bfloat16>::type;
+  extern __shared__ uint8_t few_smem[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(few_smem) + 127) & ~uintptr_t(127));
+  uint8_t* ring = base;
+  uint8_t* tok = ring + kFewStages * kFewStageBytes;
+  uint8_t* red = tok + kFewTokBytes;
+  FewShared& s = *reinterpret_cast<FewShared*>(red + kFewRedBytes);
+  cg::grid_group grid = cg::this_grid();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool worker = warp < kFewWorkers / 32;
+
+  if (tid == 0) {
+    for (int i = 0; i < kFewStages; ++i) mbar_init(&s.full[i], 1);
+    s.abort_flag = 0;
+    fence_barrier_init();
+  }
+  for (int i = tid; i < kMaxExperts; i += kFewThreads) {
+    s.mask[i] = 0;
+    s.psum[i] = 0;
+    s.counts[i] = 0;
+  }
+  if (blockIdx.x == 0 && tid == 0) *a.status = 0;
+  if (WT == kFewI8) {
+    for (int i = blockIdx.x * kFewThreads + tid; i < a.T * a.K + a.T; i += gridDim.x * kFewThreads) a.amax[i] = 0;
+  }
+  __syncthreads();
+
+  Few<WT> f(a, s, ring, tok);
+  Cursor cur;
+  uint32_t used = 0, n_units = 0;
+  if (warp == 0) {  // the shared experts' weights do not wait for the routing
+    const PassRange r = f.range(kUpShared);
+    cur.u = r.first;
+    cur.end = r.last;
+    for (int i = 0; i < kFewStages; ++i)
+      if (!few_issue(f, cur, kUpShared, lane)) break;
+  }
+  if (worker && !a.given) few_logits<X>(a, reinterpret_cast<double*>(red), tid);
+  grid.sync();
+
+  if (worker) {
+    int32_t* idx = reinterpret_cast<int32_t*>(tok);
+    float* w = reinterpret_cast<float*>(tok) + kFewMaxPairs;
+    const bool write = blockIdx.x == 0;
+    const bool with_stats = write && a.stats;
+    if (a.E <= 32)
+      few_select<1>(a, s, idx, w, with_stats, tid);
+    else if (a.E <= 64)
+      few_select<2>(a, s, idx, w, with_stats, tid);
+    else if (a.E <= 128)
+      few_select<4>(a, s, idx, w, with_stats, tid);
+    else
+      few_select<8>(a, s, idx, w, with_stats, tid);
+    named_bar_sync(1, kFewWorkers);
+    few_dispatch(a, s, idx, w, write, tid);
+    if (warp == 0) few_groups(a, s, a.ng_up, lane);
+  }
+  __syncthreads();
+  if (worker) {
+    if (warp == 0)
+      while (cur.issued < kFewStages && few_issue(f, cur, kUpRouted, lane)) {
+      }
+    few_pass(f, kUpShared, cur, used, red, n_units, kUpRouted, tid);
+    few_pass(f, kUpRouted, cur, used, red, n_units, kUpRouted, tid);
+  } else if (blockIdx.x == 0 && a.stats) {
+    // the statistics, beside the other warps' work
+    for (int e = lane; e < a.E; e += 32)
+      s.psum[e] = static_cast<unsigned long long>(__double_as_longlong(
+          balance_stats_expert(s.counts[e], s.psum[e], a.T, a.E, a.K, e, a.stats)));
+    __syncwarp();
+    if (lane == 0) {
+      balance_loss(reinterpret_cast<const double*>(s.psum), a.E, a.alpha, a.stats);
+      if (a.extended) {
+        double z = 0.0;
+        for (int i = 0; i < kFewWorkers / 32; ++i) z += s.zsum[i];
+        utilisation_stats(s.counts, s.kept, a.E, a.T, z, a.stats);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {  // the down products' groups; their first weights before the barrier
+    if (a.ng_down != a.ng_up) few_groups(a, s, a.ng_down, lane);
+    __syncwarp();
+    while (cur.issued < used + kFewStages && few_issue(f, cur, kDownRouted, lane)) {
+    }
+  }
+  grid.sync();
+  if (worker) {
+    few_pass(f, kDownShared, cur, used, red, n_units, kDownRouted, tid);
+    few_pass(f, kDownRouted, cur, used, red, n_units, kDownRouted, tid);
+  }
+  grid.sync();
+  if (worker) few_combine<X>(a, tid);
+  if (warp == 0 && s.abort_flag) {  // gave up a wait: let every copy land before the block ends
+    if (lane == 0) {
+      int never = 0;
+      for (uint32_t i = cur.issued > kFewStages ? cur.issued - kFewStages : 0; i < cur.issued; ++i)
+        mbar_wait(&s.full[i % kFewStages], (i / kFewStages) & 1u, &never);
+      raise_status(a.status, kDevWaitTimeout);
+    }
+  }
+}
+
+// ----------------------------------------------------------------- host side
+static int64_t few_pitch(int64_t bytes) { return ((bytes + 63) & ~int64_t(63)) + 16; }
+
+static size_t few_weight_bytes(const Problem& p, bool i8) { return i8 ? 1 : p.esize(); }
+
+bool few_supported(const Problem& p, bool i8) {
+  if (p.T > kFewMaxTokens) return false;
+  if (few_pitch(static_cast<int64_t>(p.d) * few_weight_bytes(p, i8)) > kFewTokBytes) return false;
+  // units are counted in 32 bits: at most one group per row
+  const int64_t rows = p.T * p.K > p.T * p.Ns ? p.T * p.K : p.T * p.Ns;
+  const int64_t lim = int64_t(1) << 31;
+  const int64_t chunks = static_cast<int64_t>(p.F) * 4 / kFewChunk + 1;
+  return rows * (p.F / 8) < lim && rows * chunks < lim && rows * chunks * (p.d / 8) < lim;
+}
+
+// Rows per token group and reduction chunks: as many rows as the token buffer
+// and the two 8-token tiles hold.  A chunk of the down product's reduction is
+// as long as leaves room for min(T, 8) rows, in whole stages.
+static void few_tiling(const Problem& p, bool i8, FewArgs* a) {
+  const int64_t ws = static_cast<int64_t>(few_weight_bytes(p, i8));
+  const int64_t most = p.dtype == kF32 && !i8 ? 8 : 16;
+  auto rows = [&](int64_t bytes) {
+    const int64_t n = kFewTokBytes / few_pitch(bytes);
+    return static_cast<int>(n < most ? n : most);
+  };
+  a->ng_up = rows(p.d * ws);
+  const int64_t fb = p.F * ws;
+  const int64_t want = p.T < 8 ? p.T : 8;
+  int64_t longest = (kFewTokBytes / want - 80) / kFewChunk * kFewChunk;
+  a->nc = static_cast<int>((fb + longest - 1) / longest);
+  const int64_t even = (fb + a->nc - 1) / a->nc;
+  const int64_t chunk = (even + kFewChunk - 1) / kFewChunk * kFewChunk;
+  a->nc = static_cast<int>((fb + chunk - 1) / chunk);
+  a->chunk_bytes = static_cast<int>(chunk);
+  a->ng_down = rows(fb < chunk ? fb : chunk);
+}
+
+FewLayout make_few_layout(const Problem& p) {
+  FewLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = (off + (bytes ? bytes : 1) + 255) & ~size_t(255);
+    return o;
+  };
+  const size_t T = static_cast<size_t>(p.T), TK = T * p.K;
+  // 8-bit weights keep the hidden rows in FP32 and may need more chunks
+  FewArgs a{}, b{};
+  few_tiling(p, false, &a);
+  few_tiling(p, true, &b);
+  const size_t nc = static_cast<size_t>(a.nc > b.nc ? a.nc : b.nc);
+  L.status = take(256);
+  L.logits = take(T * p.E * 4);
+  L.topk_idx = take(TK * 4);
+  L.topk_w = take(TK * 4);
+  L.counts = take(static_cast<size_t>(p.E) * 4);
+  L.kept = take(static_cast<size_t>(p.E) * 4);
+  L.seg_off = take(static_cast<size_t>(p.E + 1) * 4);
+  L.slot_of = take(TK * 4);
+  L.perm = take(TK * 4);
+  L.amax = take((TK + T) * 4);
+  L.h = take(TK * p.F * 4);
+  L.h_s = take(T * p.Ns * p.F * 4);
+  L.part = take(nc * TK * p.d * 4);
+  L.part_s = take(nc * T * p.Ns * p.d * 4);
+  L.total = off;
+  return L;
+}
+
+template <int WT>
+static cudaError_t run_few(const FewArgs& a, int64_t ctas, cudaStream_t st) {
+  constexpr int smem = few_smem_bytes();
+  static std::mutex mu;
+  static uint64_t done = 0;
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!((done >> dev) & 1u)) {
+      if (cudaError_t e = cudaFuncSetAttribute(few_layer_kernel<WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
+        return e;
+      done |= uint64_t(1) << dev;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_layer_kernel<WT>, a);
+}
+
+cudaError_t launch_few_layer(const Problem& p, const FewCall& c, cudaStream_t st) {
+  FewArgs a{};
+  a.x = c.x;
+  a.w_gate = c.w_gate;
+  a.logit_offset = c.logit_offset;
+  a.sel_bias = c.sel_bias;
+  a.expert_cap = c.expert_cap;
+  a.w13 = static_cast<const char*>(c.w13);
+  a.w2 = static_cast<const char*>(c.w2);
+  a.w13_s = static_cast<const char*>(c.w13_s);
+  a.w2_s = static_cast<const char*>(c.w2_s);
+  a.s13 = c.s13;
+  a.s2 = c.s2;
+  a.s13_s = c.s13_s;
+  a.s2_s = c.s2_s;
+  a.y = c.y;
+  a.logits = c.logits;
+  a.topk_idx = c.topk_idx;
+  a.topk_w = c.topk_w;
+  a.counts = c.counts;
+  a.kept = c.kept;
+  a.seg_off = c.seg_off;
+  a.slot_of = c.slot_of;
+  a.perm = c.perm;
+  a.stats = c.stats;
+  a.h = c.h;
+  a.h_s = c.h_s;
+  a.amax = c.amax;
+  a.part = c.part;
+  a.part_s = c.part_s;
+  a.status = c.status;
+  a.T = static_cast<int>(p.T);
+  a.d = p.d;
+  a.E = p.E;
+  a.K = p.K;
+  a.Ns = p.Ns;
+  a.F = p.F;
+  a.cap = p.cap;
+  a.given = c.given ? 1 : 0;
+  a.bias_on_logit = (p.flags & 0x2u) ? 1 : 0;
+  a.extended = (p.flags & 0x4u) ? 1 : 0;
+  a.alpha = p.alpha;
+  a.pscale = p_fixed_scale(p.T);
+  few_tiling(p, c.i8, &a);
+  // one CTA per SM, or one per unit of the smaller problems
+  const int64_t TK = p.T * p.K;
+  int64_t units = (p.F / 8) * ((TK < p.E ? TK : p.E) + (TK + a.ng_up - 1) / a.ng_up + p.Ns * ((p.T + a.ng_up - 1) / a.ng_up));
+  int64_t ctas = num_sms();
+  if (units < ctas) ctas = units;
+  if (ctas < 1) ctas = 1;
+  if (c.i8) return run_few<kFewI8>(a, ctas, st);
+  if (p.dtype == kF32) return run_few<kFewF32>(a, ctas, st);
+  return run_few<kFewBF16>(a, ctas, st);
+}
+
+}  // namespace moe

@@ -16,6 +16,8 @@ constexpr int kDispatchChunk = 256;  // tokens per block in the dispatch kernels
 constexpr int kSelectTokens = 8;     // tokens per block in the selection kernel (one per warp)
 constexpr int kMaxLogitParts = 8;    // most slices of the split-K gate GEMM
 constexpr int kMaxSegments = 256;    // moe_expert_ffn_segments
+constexpr int kFewMaxTokens = 64;    // moe_layer_forward_few: one bit per token
+constexpr int kMaxI8Reduction = 131056;  // 128 * 128 * K must stay below 2^31
 
 enum Dtype { kBF16 = 0, kF32 = 1 };
 
@@ -147,6 +149,66 @@ int launch_expert_ffn_mixed(const Problem& p, const void* x_perm, const int32_t*
 // expert_gemm.cu: gu = x W13^T (gate | up projections, BF16) for the backward
 int launch_up_projections(const Problem& p, int mode, const void* x_rows, int64_t n_rows, const int32_t* seg_off,
                           const void* w13, void* gu, unsigned* status, cudaStream_t st);
+// few.cu: the whole layer for at most kFewMaxTokens tokens in one kernel.
+// Byte offsets of its scratch in the caller's workspace (either weight type).
+struct FewLayout {
+  size_t status, logits, topk_idx, topk_w, counts, kept, seg_off, slot_of, perm;
+  size_t amax, h, h_s, part, part_s;
+  size_t total;
+};
+bool few_supported(const Problem& p, bool i8);
+FewLayout make_few_layout(const Problem& p);
+struct FewCall {
+  const void *x, *w_gate;
+  const float *logit_offset, *sel_bias;
+  const int32_t* expert_cap;  // or nullptr
+  const void *w13, *w2, *w13_s, *w2_s;
+  const float *s13, *s2, *s13_s, *s2_s;  // 8-bit weights
+  void* y;
+  float* logits;
+  int32_t* topk_idx;
+  float* topk_w;
+  int32_t *counts, *kept, *seg_off, *slot_of, *perm;
+  float* stats;  // or nullptr
+  void *h, *h_s;
+  unsigned* amax;
+  float *part, *part_s;
+  unsigned* status;
+  bool given, i8;
+};
+cudaError_t launch_few_layer(const Problem& p, const FewCall& c, cudaStream_t st);
+
+// Scratch of the 8-bit entry points (moe_i8_workspace_size).
+struct I8Layout {
+  WsLayout base;  // routing and dispatch arrays, y_perm, y_shared
+  size_t x_q, x_scale, h, amax, hq, h_scale;                    // routed rows
+  size_t xs_q, xs_scale, hs, amax_s, hsq, hs_scale;             // shared experts: all tokens
+  size_t total;
+};
+I8Layout make_i8_layout(const Problem& p);
+
+// quant.cu: each token's row to 8 bits and into the rows of its kept pairs
+// (x_q, x_scale by slot; amax cleared there), and, with n_shared, into
+// xs_q / xs_scale by token (amax_s cleared).
+cudaError_t launch_quantize_dispatch(const Problem& p, const void* x, const int32_t* slot_of, int8_t* x_q,
+                                     float* x_scale, unsigned* amax, int8_t* xs_q, float* xs_scale, unsigned* amax_s,
+                                     cudaStream_t st);
+// quant.cu: 8-bit rows (quant.cuh has the rule).  launch_quantize_hidden: FP32
+// rows whose largest magnitudes' bits are in amax; n_live (or nullptr): device
+// count of the rows to quantise, at most n_rows.
+cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t n_rows, int n_cols, int8_t* q, float* scale,
+                                 cudaStream_t st);
+cudaError_t launch_quantize_hidden(const float* h, const unsigned* amax, const int32_t* n_live, int64_t n_rows,
+                                   int n_cols, int8_t* q, float* scale, cudaStream_t st);
+// expert_gemm.cu: 8-bit products (moe_matmul_i8, moe_expert_ffn_i8); return a moe_status value
+int launch_matmul_i8(const int8_t* x, const float* x_scale, int64_t n_rows, const int32_t* seg_off, int n_groups,
+                     const int8_t* w, const float* w_scale, int N, int K, int out_dtype, void* y, unsigned* status,
+                     cudaStream_t st);
+int launch_expert_ffn_i8(const Problem& p, int mode, const int8_t* x, const float* x_scale, int64_t n_rows,
+                         const int32_t* seg_off, const int8_t* w13, const float* w13_scale, const int8_t* w2,
+                         const float* w2_scale, float* h, unsigned* amax, int8_t* hq, float* h_scale, void* y,
+                         unsigned* status, cudaStream_t st, bool amax_cleared = false);
+
 // grad_gemm.cu: backward of the expert FFNs (see there); returns a moe_status value
 // gu_ready: gu already holds the forward's gate/up projections (no recompute)
 // tail_a, tail_b: scratch of wgrad_tail_bytes each (the weight-gradient GEMMs'

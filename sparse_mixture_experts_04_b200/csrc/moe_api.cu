@@ -87,6 +87,38 @@ WsLayout make_layout(const Problem& p) {
   return L;
 }
 
+// The 8-bit layer: the routing arrays and outputs of the base layout, 8-bit
+// rows in place of its activations, and the hidden rows in FP32 between the
+// two products.
+I8Layout make_i8_layout(const Problem& p) {
+  I8Layout L{};
+  L.base = make_layout(p);
+  const size_t R = static_cast<size_t>(p.max_rows), T = static_cast<size_t>(p.T);
+  const size_t Fs = static_cast<size_t>(p.Ns) * p.F;
+  size_t off = L.base.x_perm;  // its activations start here
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align256(off + (bytes ? bytes : 1));
+    return o;
+  };
+  L.base.y_perm = take(R * p.d * p.esize());
+  L.base.y_shared = take(p.Ns > 0 ? T * p.d * p.esize() : 0);
+  L.x_q = take(R * p.d);
+  L.x_scale = take(R * 4);
+  L.h = take(R * p.F * 4);
+  L.amax = take(R * 4);
+  L.hq = take(R * p.F);
+  L.h_scale = take(R * 4);
+  L.xs_q = take(p.Ns > 0 ? T * p.d : 0);
+  L.xs_scale = take(p.Ns > 0 ? T * 4 : 0);
+  L.hs = take(T * Fs * 4);
+  L.amax_s = take(p.Ns > 0 ? T * 4 : 0);
+  L.hsq = take(T * Fs);
+  L.hs_scale = take(p.Ns > 0 ? T * 4 : 0);
+  L.total = off;
+  return L;
+}
+
 static bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
 // Validate the problem and derive cap / max_rows.  Returns MOE_OK or an error.
@@ -221,6 +253,77 @@ static int route_impl(const Problem& p, const void* x, const void* w_gate, const
   }
   if (n_kernels) *n_kernels += kernels;
   return MOE_OK;
+}
+
+// A problem of the 8-bit entry points.
+static int to_i8_problem(const moe_problem_t* q, Problem* p) {
+  if (int rc = to_problem(q, p)) return rc;
+  if (p->flags & MOE_FLAG_SAVE_GU) return MOE_ERR_INVALID_ARG;
+  if ((p->d % 16) || (p->F % 16)) return MOE_ERR_INVALID_ARG;
+  if (p->dtype != kBF16) return MOE_ERR_UNSUPPORTED;
+  const int64_t wide = static_cast<int64_t>(p->F) * (p->Ns > 0 ? p->Ns : 1);
+  if (p->d > kMaxI8Reduction || wide > kMaxI8Reduction) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+static int check_i8_ws(const Problem& p, void* ws, size_t ws_bytes) {
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < make_i8_layout(p).total) return MOE_ERR_WORKSPACE;
+  return MOE_OK;
+}
+
+// The weights of the 8-bit layer, checked.
+static int check_i8_weights(const Problem& p, const moe_weights_i8_t* w) {
+  if (!w || !w->w13 || !w->w13_scale || !w->w2 || !w->w2_scale) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w->w13) || !aligned16(w->w13_scale) || !aligned16(w->w2) || !aligned16(w->w2_scale))
+    return MOE_ERR_INVALID_ARG;
+  if (!(p.flags & MOE_FLAG_LOGITS_GIVEN) && (!w->w_gate || !aligned16(w->w_gate))) return MOE_ERR_INVALID_ARG;
+  if (p.Ns > 0) {
+    if (!w->w13_shared || !w->w13_shared_scale || !w->w2_shared || !w->w2_shared_scale) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(w->w13_shared) || !aligned16(w->w13_shared_scale) || !aligned16(w->w2_shared) ||
+        !aligned16(w->w2_shared_scale))
+      return MOE_ERR_INVALID_ARG;
+  } else if (w->w13_shared || w->w2_shared || w->w13_shared_scale || w->w2_shared_scale) {
+    return MOE_ERR_INVALID_ARG;
+  }
+  if ((p.flags & MOE_FLAG_EXPERT_CAPACITY) && (!w->expert_capacity || !aligned16(w->expert_capacity)))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// moe_layer_forward_few and its 8-bit form, after the weights were checked.
+static int few_impl(const Problem& p, FewCall c, const void* x, void* y, const moe_routing_t* routing, float* stats,
+                    void* ws, size_t ws_bytes, moe_stream_t stream) {
+  const bool given = p.flags & MOE_FLAG_LOGITS_GIVEN;
+  if (!x || !y || !aligned16(x) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  if (given && (!routing || !routing->logits)) return MOE_ERR_INVALID_ARG;
+  if (!few_supported(p, c.i8)) return MOE_ERR_UNSUPPORTED;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_WORKSPACE;
+  const FewLayout L = make_few_layout(p);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  moe_routing_t r{};
+  if (routing) r = *routing;
+  c.x = x;
+  c.y = y;
+  c.given = given;
+  if (given) c.logit_offset = nullptr;
+  if (!(p.flags & MOE_FLAG_EXPERT_CAPACITY)) c.expert_cap = nullptr;
+  c.logits = r.logits ? r.logits : at<float>(ws, L.logits);
+  c.topk_idx = r.topk_idx ? r.topk_idx : at<int32_t>(ws, L.topk_idx);
+  c.topk_w = r.topk_w ? r.topk_w : at<float>(ws, L.topk_w);
+  c.counts = r.counts ? r.counts : at<int32_t>(ws, L.counts);
+  c.kept = r.kept ? r.kept : at<int32_t>(ws, L.kept);
+  c.seg_off = r.seg_off ? r.seg_off : at<int32_t>(ws, L.seg_off);
+  c.slot_of = r.slot_of ? r.slot_of : at<int32_t>(ws, L.slot_of);
+  c.perm = r.perm ? r.perm : at<int32_t>(ws, L.perm);
+  c.stats = stats;
+  c.h = at<void>(ws, L.h);
+  c.h_s = at<void>(ws, L.h_s);
+  c.amax = at<unsigned>(ws, L.amax);
+  c.part = at<float>(ws, L.part);
+  c.part_s = at<float>(ws, L.part_s);
+  c.status = at<unsigned>(ws, L.status);
+  return cuda_rc(launch_few_layer(p, c, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace moe
@@ -542,6 +645,177 @@ int moe_layer_forward_clocked(const moe_problem_t* q, const void* x, const moe_w
   static_assert(sizeof(unsigned long long) == sizeof(uint64_t), "64-bit clocks");
   return layer_forward_impl(q, x, w, y, routing, stats, ws, ws_bytes, stream, nullptr, nullptr,
                             reinterpret_cast<unsigned long long*>(clocks));
+}
+
+int moe_few_workspace_size(const moe_problem_t* q, size_t* bytes) {
+  Problem p;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  if (int rc = to_problem(q, &p)) return rc;
+  if (!few_supported(p, false) && !few_supported(p, true)) return MOE_ERR_UNSUPPORTED;
+  *bytes = make_few_layout(p).total;
+  return MOE_OK;
+}
+
+int moe_layer_forward_few(const moe_problem_t* q, const void* x, const moe_weights_t* w, void* y,
+                          const moe_routing_t* routing, float* stats, void* ws, size_t ws_bytes,
+                          moe_stream_t stream) {
+  Problem p;
+  if (int rc = to_problem(q, &p)) return rc;
+  if (p.flags & MOE_FLAG_SAVE_GU) return MOE_ERR_INVALID_ARG;
+  if (!w || !w->w13 || !w->w2 || !aligned16(w->w13) || !aligned16(w->w2)) return MOE_ERR_INVALID_ARG;
+  if (!(p.flags & MOE_FLAG_LOGITS_GIVEN) && (!w->w_gate || !aligned16(w->w_gate))) return MOE_ERR_INVALID_ARG;
+  if (p.Ns > 0 && (!w->w13_shared || !w->w2_shared || !aligned16(w->w13_shared) || !aligned16(w->w2_shared)))
+    return MOE_ERR_INVALID_ARG;
+  if (p.Ns == 0 && (w->w13_shared || w->w2_shared)) return MOE_ERR_INVALID_ARG;
+  if ((p.flags & MOE_FLAG_EXPERT_CAPACITY) && (!w->expert_capacity || !aligned16(w->expert_capacity)))
+    return MOE_ERR_INVALID_ARG;
+  FewCall c{};
+  c.w_gate = w->w_gate;
+  c.logit_offset = w->logit_offset;
+  c.sel_bias = w->sel_bias;
+  c.expert_cap = w->expert_capacity;
+  c.w13 = w->w13;
+  c.w2 = w->w2;
+  c.w13_s = w->w13_shared;
+  c.w2_s = w->w2_shared;
+  return few_impl(p, c, x, y, routing, stats, ws, ws_bytes, stream);
+}
+
+int moe_layer_forward_few_i8(const moe_problem_t* q, const void* x, const moe_weights_i8_t* w, void* y,
+                             const moe_routing_t* routing, float* stats, void* ws, size_t ws_bytes,
+                             moe_stream_t stream) {
+  Problem p;
+  if (int rc = to_i8_problem(q, &p)) return rc;
+  if (int rc = check_i8_weights(p, w)) return rc;
+  FewCall c{};
+  c.i8 = true;
+  c.w_gate = w->w_gate;
+  c.logit_offset = w->logit_offset;
+  c.sel_bias = w->sel_bias;
+  c.expert_cap = w->expert_capacity;
+  c.w13 = w->w13;
+  c.w2 = w->w2;
+  c.w13_s = w->w13_shared;
+  c.w2_s = w->w2_shared;
+  c.s13 = w->w13_scale;
+  c.s2 = w->w2_scale;
+  c.s13_s = w->w13_shared_scale;
+  c.s2_s = w->w2_shared_scale;
+  return few_impl(p, c, x, y, routing, stats, ws, ws_bytes, stream);
+}
+
+int moe_quantize_rows(int64_t n_rows, int32_t n_cols, int32_t dtype, const void* x, int8_t* x_q, float* x_scale,
+                      moe_stream_t stream) {
+  if (n_rows < 1 || n_cols < 16 || (n_cols % 16)) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+  if (!x || !x_q || !x_scale || !aligned16(x) || !aligned16(x_q) || !aligned16(x_scale)) return MOE_ERR_INVALID_ARG;
+  return cuda_rc(launch_quantize_rows(dtype, x, n_rows, n_cols, x_q, x_scale, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_matmul_i8(int32_t n_groups, int64_t n_rows, int32_t N, int32_t K, const int8_t* x, const float* x_scale,
+                  const int32_t* seg_off, const int8_t* w, const float* w_scale, int32_t out_dtype, void* y, void* ws,
+                  size_t ws_bytes, moe_stream_t stream) {
+  if (n_groups < 1 || n_rows < 1 || N < 8 || (N % 8) || K < 16 || (K % 16)) return MOE_ERR_INVALID_ARG;
+  if (out_dtype != MOE_DTYPE_BF16 && out_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+  if (!x || !x_scale || !w || !w_scale || !y || (!seg_off && n_groups != 1)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(x_scale) || !aligned16(w) || !aligned16(w_scale) || !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  if (n_groups > 256 || K > kMaxI8Reduction || n_rows >= (static_cast<int64_t>(1) << 31) - 256 ||
+      static_cast<int64_t>(N) * n_groups >= (static_cast<int64_t>(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < MOE_MATMUL_WORKSPACE) return MOE_ERR_WORKSPACE;
+  return launch_matmul_i8(x, x_scale, n_rows, seg_off, n_groups, w, w_scale, N, K, out_dtype, y,
+                          at<unsigned>(ws, 0), reinterpret_cast<cudaStream_t>(stream))
+             ? MOE_ERR_CUDA
+             : MOE_OK;
+}
+
+int moe_i8_workspace_size(const moe_problem_t* q, size_t* bytes) {
+  Problem p;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  if (int rc = to_i8_problem(q, &p)) return rc;
+  *bytes = make_i8_layout(p).total;
+  return MOE_OK;
+}
+
+int moe_expert_ffn_i8(const moe_problem_t* q, int32_t mode, const int8_t* x_rows, const float* x_scale,
+                      int64_t n_rows, const int32_t* seg_off, const int8_t* w13, const float* w13_scale,
+                      const int8_t* w2, const float* w2_scale, void* y_rows, void* ws, size_t ws_bytes,
+                      moe_stream_t stream) {
+  Problem p;
+  if (int rc = to_i8_problem(q, &p)) return rc;
+  if (int rc = check_i8_ws(p, ws, ws_bytes)) return rc;
+  if (mode != MOE_FFN_ROUTED && mode != MOE_FFN_SHARED) return MOE_ERR_INVALID_ARG;
+  if (!x_rows || !x_scale || !w13 || !w13_scale || !w2 || !w2_scale || !y_rows || n_rows < 1)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x_rows) || !aligned16(x_scale) || !aligned16(w13) || !aligned16(w13_scale) || !aligned16(w2) ||
+      !aligned16(w2_scale) || !aligned16(y_rows))
+    return MOE_ERR_INVALID_ARG;
+  if (mode == MOE_FFN_ROUTED && (!seg_off || n_rows > p.max_rows)) return MOE_ERR_INVALID_ARG;
+  if (mode == MOE_FFN_SHARED && (p.Ns < 1 || n_rows > p.T)) return MOE_ERR_INVALID_ARG;
+  const I8Layout L = make_i8_layout(p);
+  const bool routed = mode == MOE_FFN_ROUTED;
+  return launch_expert_ffn_i8(p, mode, x_rows, x_scale, n_rows, seg_off, w13, w13_scale, w2, w2_scale,
+                              at<float>(ws, routed ? L.h : L.hs), at<unsigned>(ws, routed ? L.amax : L.amax_s),
+                              at<int8_t>(ws, routed ? L.hq : L.hsq), at<float>(ws, routed ? L.h_scale : L.hs_scale),
+                              y_rows, at<unsigned>(ws, L.base.status), reinterpret_cast<cudaStream_t>(stream))
+             ? MOE_ERR_CUDA
+             : MOE_OK;
+}
+
+int moe_layer_forward_i8(const moe_problem_t* q, const void* x, const moe_weights_i8_t* w, void* y,
+                         const moe_routing_t* routing, float* stats, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  Problem p;
+  if (int rc = to_i8_problem(q, &p)) return rc;
+  if (int rc = check_i8_ws(p, ws, ws_bytes)) return rc;
+  if (int rc = check_i8_weights(p, w)) return rc;
+  const bool given = p.flags & MOE_FLAG_LOGITS_GIVEN;
+  if (!x || !y || !aligned16(x) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  if (given && (!routing || !routing->logits)) return MOE_ERR_INVALID_ARG;
+  const int32_t* expert_cap = (p.flags & MOE_FLAG_EXPERT_CAPACITY) ? w->expert_capacity : nullptr;
+  const I8Layout L = make_i8_layout(p);
+  const WsLayout& B = L.base;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  moe_routing_t r{};
+  if (routing) r = *routing;
+  float* logits = r.logits ? r.logits : at<float>(ws, B.logits);
+  int32_t* idx = r.topk_idx ? r.topk_idx : at<int32_t>(ws, B.topk_idx);
+  float* gw = r.topk_w ? r.topk_w : at<float>(ws, B.topk_w);
+  int32_t* counts = r.counts ? r.counts : at<int32_t>(ws, B.counts);
+  int32_t* kept = r.kept ? r.kept : at<int32_t>(ws, B.kept);
+  int32_t* seg_off = r.seg_off ? r.seg_off : at<int32_t>(ws, B.seg_off);
+  int32_t* slot_of = r.slot_of ? r.slot_of : at<int32_t>(ws, B.slot_of);
+  int32_t* perm = r.perm ? r.perm : at<int32_t>(ws, B.perm);
+  unsigned* status = at<unsigned>(ws, B.status);
+  if (cudaError_t e = cudaMemsetAsync(ws, 0, B.zero_bytes, st)) return cuda_rc(e);
+  int n_zpart = 0;
+  if (int rc = route_impl(p, x, w->w_gate, given ? nullptr : w->logit_offset, w->sel_bias, logits, idx, gw, stats, ws,
+                          B, st, /*chunk_totals_cleared=*/true, /*stats_in_route=*/false, &n_zpart, nullptr))
+    return rc;
+  if (cudaError_t e = launch_dispatch(p, idx, counts, kept, seg_off, slot_of, perm, at<int32_t>(ws, B.chunk_counts),
+                                      at<int32_t>(ws, B.chunk_base), status, st, /*counts_ready=*/true,
+                                      at<unsigned long long>(ws, B.chunk_psum), stats,
+                                      (stats && (p.flags & MOE_FLAG_EXTENDED_STATS)) ? at<float>(ws, B.zpart) : nullptr,
+                                      n_zpart, expert_cap))
+    return cuda_rc(e);
+  const bool shared = p.Ns > 0;
+  if (cudaError_t e = launch_quantize_dispatch(p, x, slot_of, at<int8_t>(ws, L.x_q), at<float>(ws, L.x_scale),
+                                               at<unsigned>(ws, L.amax), shared ? at<int8_t>(ws, L.xs_q) : nullptr,
+                                               at<float>(ws, L.xs_scale), at<unsigned>(ws, L.amax_s), st))
+    return cuda_rc(e);
+  if (p.max_rows > 0 &&
+      launch_expert_ffn_i8(p, MOE_FFN_ROUTED, at<int8_t>(ws, L.x_q), at<float>(ws, L.x_scale), p.max_rows, seg_off,
+                           w->w13, w->w13_scale, w->w2, w->w2_scale, at<float>(ws, L.h), at<unsigned>(ws, L.amax),
+                           at<int8_t>(ws, L.hq), at<float>(ws, L.h_scale), at<void>(ws, B.y_perm), status, st, true))
+    return MOE_ERR_CUDA;
+  if (shared &&
+      launch_expert_ffn_i8(p, MOE_FFN_SHARED, at<int8_t>(ws, L.xs_q), at<float>(ws, L.xs_scale), p.T, nullptr,
+                           w->w13_shared, w->w13_shared_scale, w->w2_shared, w->w2_shared_scale, at<float>(ws, L.hs),
+                           at<unsigned>(ws, L.amax_s), at<int8_t>(ws, L.hsq), at<float>(ws, L.hs_scale),
+                           at<void>(ws, B.y_shared), status, st, true))
+    return MOE_ERR_CUDA;
+  return cuda_rc(launch_combine(p, at<void>(ws, B.y_perm), slot_of, gw, shared ? at<void>(ws, B.y_shared) : nullptr, y,
+                                st));
 }
 
 }  // extern "C"

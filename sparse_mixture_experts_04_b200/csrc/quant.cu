@@ -1,0 +1,210 @@
+// Row quantisation to 8-bit integers (see quant.cuh for the rule).
+//
+//   quantize_rows_kernel    x [n, c] BF16 or FP32 -> q [n, c] int8, scale [n]
+//   quantize_hidden_kernel  the SwiGLU outputs of the 8-bit up projection, FP32
+//                           with each row's largest magnitude already known
+//
+// Both are bound by memory: one read of the row, one write of a byte per
+// element.
+#include "common.cuh"
+#include "internal.h"
+#include "quant.cuh"
+
+namespace moe {
+
+constexpr int kQuantThreads = 256;
+
+// One block per row.  A thread keeps up to kQuantKeep 16-element pieces of its
+// row in registers between the maximum and the rounding; longer rows are read
+// again (from L2).
+constexpr int kQuantKeep = 2;
+
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, float (&v)[16]);
+template <>
+__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[16]) {
+  const uint4* q = reinterpret_cast<const uint4*>(p);
+  const uint4 a = q[0], b = q[1];
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+template <>
+__device__ __forceinline__ void load16<float>(const float* p, float (&v)[16]) {
+  const float4* q = reinterpret_cast<const float4*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 a = q[i];
+    v[4 * i] = a.x; v[4 * i + 1] = a.y; v[4 * i + 2] = a.z; v[4 * i + 3] = a.w;
+  }
+}
+
+__device__ __forceinline__ uint4 quant_pack16(const float (&v)[16], float scale, float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float f[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+    w[i] = quant_pack4(f, scale, inv);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ unsigned block_max_u32(unsigned v, unsigned* s_max) {
+  v = warp_max_u32(v);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = v;
+  __syncthreads();
+  unsigned m = 0;
+#pragma unroll
+  for (int w = 0; w < kQuantThreads / 32; ++w) m = max(m, s_max[w]);
+  __syncthreads();
+  return m;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const T* __restrict__ x, int64_t n_rows,
+                                                                      int n_cols, int8_t* __restrict__ q,
+                                                                      float* __restrict__ scale) {
+  __shared__ unsigned s_max[kQuantThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int pieces = n_cols / 16;
+  for (int64_t row = blockIdx.x; row < n_rows; row += gridDim.x) {
+    const T* xr = x + row * n_cols;
+    int8_t* qr = q + row * n_cols;
+    float v[kQuantKeep][16];
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < kQuantKeep; ++i) {
+      const int p = threadIdx.x + i * kQuantThreads;
+      if (p < pieces) {
+        load16(xr + p * 16, v[i]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m = max(m, abs_bits(v[i][j]));
+      }
+    }
+    for (int p = threadIdx.x + kQuantKeep * kQuantThreads; p < pieces; p += kQuantThreads) {
+      float t[16];
+      load16(xr + p * 16, t);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) m = max(m, abs_bits(t[j]));
+    }
+    const float s = quant_scale(block_max_u32(m, s_max));
+    const float inv = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < kQuantKeep; ++i) {
+      const int p = threadIdx.x + i * kQuantThreads;
+      if (p < pieces) *reinterpret_cast<uint4*>(qr + p * 16) = quant_pack16(v[i], s, inv);
+    }
+    for (int p = threadIdx.x + kQuantKeep * kQuantThreads; p < pieces; p += kQuantThreads) {
+      float t[16];
+      load16(xr + p * 16, t);
+      *reinterpret_cast<uint4*>(qr + p * 16) = quant_pack16(t, s, inv);
+    }
+    if (threadIdx.x == 0) scale[row] = s;
+  }
+}
+
+cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t n_rows, int n_cols, int8_t* q, float* scale,
+                                 cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>(n_rows < 65536 ? n_rows : 65536);
+  if (dtype == kBF16)
+    return launch_k(quantize_rows_kernel<__nv_bfloat16>, dim3(grid), dim3(kQuantThreads), 0, st,
+                    static_cast<const __nv_bfloat16*>(x), n_rows, n_cols, q, scale);
+  return launch_k(quantize_rows_kernel<float>, dim3(grid), dim3(kQuantThreads), 0, st, static_cast<const float*>(x),
+                  n_rows, n_cols, q, scale);
+}
+
+// One block per token: the row is read once, its 8 bits go to every kept pair's
+// row (a token is stored up to K + 1 times, read once).
+__global__ void __launch_bounds__(kQuantThreads) quantize_dispatch_kernel(
+    const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ slot_of, int64_t T, int d, int K,
+    int64_t max_rows, int8_t* __restrict__ x_q, float* __restrict__ x_scale, unsigned* __restrict__ amax,
+    int8_t* __restrict__ xs_q, float* __restrict__ xs_scale, unsigned* __restrict__ amax_s) {
+  __shared__ unsigned s_max[kQuantThreads / 32];
+  __shared__ int s_slot[kMaxTopK];
+  pdl_wait();
+  pdl_trigger();
+  const int pieces = d / 16;
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+    const __nv_bfloat16* xr = x + t * d;
+    if (threadIdx.x < K) {
+      const int sl = slot_of[t * K + threadIdx.x];
+      s_slot[threadIdx.x] = sl < max_rows ? sl : -1;
+    }
+    unsigned m = 0;
+    for (int p = threadIdx.x; p < pieces; p += kQuantThreads) {
+      float v[16];
+      load16(xr + p * 16, v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) m = max(m, abs_bits(v[j]));
+    }
+    const float s = quant_scale(block_max_u32(m, s_max));
+    const float inv = 1.0f / s;
+    for (int p = threadIdx.x; p < pieces; p += kQuantThreads) {
+      float v[16];
+      load16(xr + p * 16, v);
+      const uint4 w = quant_pack16(v, s, inv);
+      for (int k = 0; k < K; ++k)
+        if (s_slot[k] >= 0) *reinterpret_cast<uint4*>(x_q + static_cast<int64_t>(s_slot[k]) * d + p * 16) = w;
+      if (xs_q) *reinterpret_cast<uint4*>(xs_q + t * d + p * 16) = w;
+    }
+    if (threadIdx.x < K && s_slot[threadIdx.x] >= 0) {
+      x_scale[s_slot[threadIdx.x]] = s;
+      amax[s_slot[threadIdx.x]] = 0;
+    }
+    if (threadIdx.x == 0 && xs_q) {
+      xs_scale[t] = s;
+      amax_s[t] = 0;
+    }
+    __syncthreads();
+  }
+}
+
+cudaError_t launch_quantize_dispatch(const Problem& p, const void* x, const int32_t* slot_of, int8_t* x_q,
+                                     float* x_scale, unsigned* amax, int8_t* xs_q, float* xs_scale, unsigned* amax_s,
+                                     cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>(p.T < 65536 ? p.T : 65536);
+  return launch_k(quantize_dispatch_kernel, dim3(grid), dim3(kQuantThreads), 0, st,
+                  static_cast<const __nv_bfloat16*>(x), slot_of, p.T, p.d, p.K, p.max_rows, x_q, x_scale, amax, xs_q,
+                  xs_scale, amax_s);
+}
+
+// h [*, n_cols] FP32, amax [*] bits of each row's largest magnitude; rows
+// [0, min(*n_live, n_rows)) (n_live NULL: n_rows)
+__global__ void __launch_bounds__(kQuantThreads) quantize_hidden_kernel(const float* __restrict__ h,
+                                                                        const unsigned* __restrict__ amax,
+                                                                        const int32_t* __restrict__ n_live,
+                                                                        int n_rows, int n_cols,
+                                                                        int8_t* __restrict__ q,
+                                                                        float* __restrict__ scale) {
+  pdl_wait();
+  pdl_trigger();
+  const int rows = n_live ? min(max(*n_live, 0), n_rows) : n_rows;
+  const int pieces = n_cols / 16;
+  const int64_t total = static_cast<int64_t>(rows) * pieces;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int row = static_cast<int>(i / pieces);
+    const int p = static_cast<int>(i - static_cast<int64_t>(row) * pieces);
+    const float s = quant_scale(amax[row]);
+    float v[16];
+    load16(h + static_cast<int64_t>(row) * n_cols + p * 16, v);
+    *reinterpret_cast<uint4*>(q + static_cast<int64_t>(row) * n_cols + p * 16) = quant_pack16(v, s, 1.0f / s);
+    if (p == 0) scale[row] = s;
+  }
+}
+
+cudaError_t launch_quantize_hidden(const float* h, const unsigned* amax, const int32_t* n_live, int64_t n_rows,
+                                   int n_cols, int8_t* q, float* scale, cudaStream_t st) {
+  const int64_t pieces = n_rows * (n_cols / 16);
+  int64_t grid = (pieces + kQuantThreads - 1) / kQuantThreads;
+  const int64_t most = static_cast<int64_t>(num_sms()) * 8;
+  if (grid > most) grid = most;
+  return launch_k(quantize_hidden_kernel, dim3(static_cast<unsigned>(grid)), dim3(kQuantThreads), 0, st, h, amax,
+                  n_live, static_cast<int>(n_rows), n_cols, q, scale);
+}
+
+}  // namespace moe

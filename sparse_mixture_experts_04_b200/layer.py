@@ -10,11 +10,17 @@ from . import api
 
 
 class MoeLayer:
+    # the C entry points behind the methods (MoeLayerI8 has its own)
+    _alloc_workspace = staticmethod(api.alloc_workspace)
+    _forward = staticmethod(api.moe_layer_forward)
+    _forward_few = staticmethod(api.moe_layer_forward_few)
+
     def __init__(self, prob: api.MoeProblem, weights: dict, device="cuda", keep_routing: bool = True):
         self.prob = prob
         self.device = torch.device(device)
         self.weights = weights
-        self.ws = api.alloc_workspace(prob, self.device)
+        self.ws = self._alloc_workspace(prob, self.device)
+        self.few_ws = None  # forward_few's workspace, allocated by its first call
         self.dtype = torch.bfloat16 if prob.dtype == api.DTYPE_BF16 else torch.float32
         T, E, K = prob.T, prob.n_experts, prob.top_k
         self.routing = None
@@ -57,11 +63,25 @@ class MoeLayer:
                 stream=None) -> torch.Tensor:
         if y is None:
             y = torch.empty((self.prob.T, self.prob.d_model), dtype=self.dtype, device=self.device)
-        api.moe_layer_forward(self.prob, x, self.weights, y, self.routing, self.stats if with_stats else None,
-                              self.ws, stream)
+        self._forward(self.prob, x, self.weights, y, self.routing, self.stats if with_stats else None, self.ws, stream)
         return y
 
     __call__ = forward
+
+    def forward_few(self, x: torch.Tensor, y: torch.Tensor | None = None, with_stats: bool = True,
+                    stream=None) -> torch.Tensor:
+        """forward() in one kernel, for layers of at most api.FEW_MAX_TOKENS
+        tokens (decode steps): same inputs, outputs, routing and statistics.
+        Agrees with forward() to rounding (its expert outputs are not rounded
+        before the combine).  No backward() from it: that reads what forward()
+        leaves behind.  Its device status is in self.few_ws."""
+        if y is None:
+            y = torch.empty((self.prob.T, self.prob.d_model), dtype=self.dtype, device=self.device)
+        if self.few_ws is None:
+            self.few_ws = api.alloc_few_workspace(self.prob, self.device)
+        self._forward_few(self.prob, x, self.weights, y, self.routing, self.stats if with_stats else None,
+                          self.few_ws, stream)
+        return y
 
     def capture(self, with_stats: bool = True) -> None:
         """Capture one forward into a CUDA graph over static input/output
@@ -77,8 +97,8 @@ class MoeLayer:
         torch.cuda.synchronize(self.device)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            api.moe_layer_forward(self.prob, self.graph_x, self.weights, self.graph_y, self.routing,
-                                  self.stats if with_stats else None, self.ws)
+            self._forward(self.prob, self.graph_x, self.weights, self.graph_y, self.routing,
+                          self.stats if with_stats else None, self.ws)
         self._graph = g
 
     def forward_graphed(self, x: torch.Tensor | None = None) -> torch.Tensor:
@@ -173,7 +193,7 @@ class MoeLayer:
             comp.wait_event(copied_in[i])
             if i >= 2:
                 comp.wait_event(copied_out[i - 2])        # y / stats buffers b are free again
-            api.moe_layer_forward(self.prob, xb[b], self.weights, yb[b], self.routing, sb[b], self.ws, comp)
+            self._forward(self.prob, xb[b], self.weights, yb[b], self.routing, sb[b], self.ws, comp)
             computed[i].record(comp)
             with torch.cuda.stream(d2h):
                 d2h.wait_event(computed[i])
@@ -183,3 +203,44 @@ class MoeLayer:
                 copied_out[i].record(d2h)
         comp.wait_stream(d2h)
         comp.synchronize()
+
+
+def quantize_weights(weights: dict) -> dict:
+    """The weights of a layer (w13, w2 and the shared ones, BF16 or FP32, on a
+    CUDA device) to 8 bits with a scale per output channel, for MoeLayerI8; the
+    router's arrays and expert_capacity are passed on.  The shared experts are
+    one expert of width N_s * F: w2_shared has one scale per output channel
+    over all of them."""
+    out = {k: weights.get(k) for k in ("w_gate", "logit_offset", "sel_bias", "expert_capacity")}
+    for k in ("w13", "w2", "w13_shared"):
+        if weights.get(k) is not None:
+            out[k], out[k + "_scale"] = api.quantize_rows(weights[k])
+    w2s = weights.get("w2_shared")
+    if w2s is not None:
+        n, d, F = w2s.shape
+        q, out["w2_shared_scale"] = api.quantize_rows(w2s.permute(1, 0, 2).reshape(d, n * F).contiguous())
+        out["w2_shared"] = q.view(d, n, F).permute(1, 0, 2).contiguous()
+    return out
+
+
+class MoeLayerI8(MoeLayer):
+    """MoeLayer with 8-bit experts: the same forward(), forward_few(), capture()
+    and balance_update() over weights from quantize_weights (or the caller's
+    own int8 matrices and scales; see moe_weights_i8_t in the header).  Token
+    rows and hidden rows are quantised on the way.  BF16 activations, d_model
+    and d_ff multiples of 16.  Inference only."""
+    _alloc_workspace = staticmethod(api.alloc_i8_workspace)
+    _forward = staticmethod(api.moe_layer_forward_i8)
+    _forward_few = staticmethod(api.moe_layer_forward_few_i8)
+
+    @classmethod
+    def from_layer(cls, layer: MoeLayer, keep_routing: bool = True) -> "MoeLayerI8":
+        """Quantise an existing layer's weights (the layer keeps its own)."""
+        return cls(layer.prob, quantize_weights(layer.weights), layer.device, keep_routing)
+
+    @classmethod
+    def from_inputs(cls, inputs: dict, device="cuda", flags: int = 0, keep_routing: bool = True) -> "MoeLayerI8":
+        return cls.from_layer(MoeLayer.from_inputs(inputs, device, flags, False), keep_routing)
+
+    def backward(self, *args, **kwargs):
+        raise RuntimeError("8-bit experts have no backward: train with MoeLayer and quantise its weights")
