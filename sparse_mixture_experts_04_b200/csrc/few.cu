@@ -52,7 +52,7 @@ namespace cg = cooperative_groups;
 enum { kFewBF16 = 0, kFewF32 = 1, kFewI8 = 2 };
 
 constexpr int kFewWorkers = 256;                 // 8 warps
-constexpr int kFewThreads = kFewWorkers + 32;    // + one warp for the statistics
+constexpr int kFewThreads = kFewWorkers + 64;    // + a warp for the copies, a warp for the statistics
 constexpr int kFewRows = 16;                     // weight rows of a unit
 constexpr int kFewChunk = 2048;                  // bytes of each row in a stage
 constexpr int kFewPitch = kFewChunk + 16;        // odd number of 16-byte pieces: no bank conflicts
@@ -64,13 +64,14 @@ constexpr int kFewRedBytes = 2 * 8 * 2 * 128 * 4;  // [2][8 warps][2 token tiles
 
 struct FewShared {
   uint64_t full[kFewStages];
+  uint64_t empty[kFewStages];
   unsigned long long mask[kMaxExperts];   // tokens that chose the expert
   unsigned long long psum[kMaxExperts];   // sum of p, fixed point; then f_e P_e as doubles (statistics)
   double zsum[8];
   int counts[kMaxExperts];
   int kept[kMaxExperts];
   int seg_off[kMaxExperts + 1];
-  int groups[kMaxExperts + 1];            // prefix of the experts' token groups
+  int groups[2][kMaxExperts + 1];         // prefix of the experts' token groups: up, down
   uint16_t perm[kFewMaxPairs];            // slot -> t * K + k
   float row_scale[16];                    // 8-bit tokens: scale of each row in the token buffer
   int abort_flag;
@@ -161,17 +162,18 @@ struct PassRange {
   int first, last;  // units [first, last)
 };
 
-// A unit, decoded: which weights, which tokens.
-struct Unit {
-  const char* w;       // row 0 of the unit at the start of its reduction
+// A run of units over the same tokens, decoded: which weights, which tokens.
+struct Span {
+  const char* w;       // row 0 of the current unit at the start of its reduction
   int64_t hi;          // byte offset from row r < 8 to row r + 8
   int64_t row_bytes;   // distance between rows
-  int rows;            // valid rows: 16, or 8 at the end of d
+  int units;           // units of the span
+  int step;            // features (up: 8) or output channels (down: 16) of a unit
+  int col, cols;       // first feature / channel of the current unit, and their number in all
   int len;             // bytes of each row in the unit's reduction
   int e;               // expert (routed or shared)
   int row0, n;         // first token row (slot or token) and their number
   int c;               // reduction chunk (down)
-  int col;             // first feature / output channel
 };
 
 template <int WT>
@@ -193,12 +195,12 @@ struct Few {
   // token groups of the shared experts / of the routed ones, for rows per group ng
   __device__ __forceinline__ int shared_groups(int ng) const { return (a.T + ng - 1) / ng; }
 
-  // units of a pass (routed passes: s.groups is the up or the down prefix)
+  // units of a pass
   __device__ __forceinline__ int64_t units(int pass) const {
     if (pass == kUpShared) return static_cast<int64_t>(a.Ns) * shared_groups(a.ng_up) * nfb;
-    if (pass == kUpRouted) return static_cast<int64_t>(s.groups[a.E]) * nfb;
+    if (pass == kUpRouted) return static_cast<int64_t>(s.groups[0][a.E]) * nfb;
     if (pass == kDownShared) return static_cast<int64_t>(a.Ns) * a.nc * shared_groups(a.ng_down) * nb;
-    return static_cast<int64_t>(s.groups[a.E]) * a.nc * nb;
+    return static_cast<int64_t>(s.groups[1][a.E]) * a.nc * nb;
   }
   __device__ __forceinline__ PassRange range(int pass) const {
     const int64_t n = units(pass);
@@ -206,27 +208,28 @@ struct Few {
   }
 
   // expert of routed token group v (largest e with groups[e] <= v that has groups)
-  __device__ __forceinline__ int group_expert(int v) const {
+  __device__ __forceinline__ int group_expert(const int* groups, int v) const {
     int lo = 0, hi = a.E - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (s.groups[mid] <= v) lo = mid; else hi = mid - 1;
+      if (groups[mid] <= v) lo = mid; else hi = mid - 1;
     }
     return lo;
   }
 
-  __device__ __forceinline__ Unit unit(int pass, int u) const {
-    Unit q;
+  // The span that unit u begins or lies in: its units share tokens, expert and
+  // reduction chunk, and differ by their rows.
+  __device__ __forceinline__ Span span(int pass, int u, int last) const {
+    Span q;
     const bool up = pass <= kUpRouted;
     const int ng = up ? a.ng_up : a.ng_down;
-    int v, blk;
-    if (up) {
-      v = u / nfb;
-      blk = u - v * nfb;
-      q.c = 0;
-    } else {
-      const int t = u / nb;
-      blk = u - t * nb;
+    const int per = up ? nfb : nb;
+    int v = u / per;
+    const int blk = u - v * per;
+    q.units = min(per - blk, last - u);
+    q.c = 0;
+    if (!up) {
+      const int t = v;
       v = t / a.nc;
       q.c = t - v * a.nc;
     }
@@ -238,22 +241,25 @@ struct Few {
       q.n = min(ng, a.T - q.row0);
       base = up ? a.w13_s : a.w2_s;
     } else {
-      q.e = group_expert(v);
-      q.row0 = s.seg_off[q.e] + (v - s.groups[q.e]) * ng;
+      const int* groups = s.groups[up ? 0 : 1];
+      q.e = group_expert(groups, v);
+      q.row0 = s.seg_off[q.e] + (v - groups[q.e]) * ng;
       q.n = min(ng, s.seg_off[q.e + 1] - q.row0);
       base = up ? a.w13 : a.w2;
     }
     if (up) {
       q.row_bytes = static_cast<int64_t>(a.d) * kW;
+      q.step = 8;
       q.col = blk * 8;
-      q.rows = 16;
+      q.cols = a.F;
       q.len = a.d * kW;
       q.hi = a.F * q.row_bytes;
       q.w = base + (static_cast<int64_t>(q.e) * 2 * a.F + q.col) * q.row_bytes;
     } else {
       q.row_bytes = static_cast<int64_t>(a.F) * kW;
+      q.step = kFewRows;
       q.col = blk * kFewRows;
-      q.rows = min(kFewRows, a.d - q.col);
+      q.cols = a.d;
       const int64_t k0 = static_cast<int64_t>(q.c) * a.chunk_bytes;
       q.len = static_cast<int>(min(static_cast<int64_t>(a.chunk_bytes), q.row_bytes - k0));
       q.hi = 8 * q.row_bytes;
@@ -263,51 +269,55 @@ struct Few {
   }
 };
 
-// The copy side of the ring: the next stage to fill, walked in the order in
-// which the stages are consumed.  Kept by every lane of warp 0 alike.
+// The copy side of the ring (one warp, every lane alike): the stages are
+// filled in the order in which they are consumed.
 struct Cursor {
-  int pass = 0, u = 0, end = 0, off = 0;
-  bool loaded = false;   // cur holds unit u
-  uint32_t issued = 0;   // stages filled so far
-  Unit cur;
+  int pass = 0, u = 0, end = 0;  // next unit of the pass, the pass's last
+  int left = 0, off = 0;         // units left in the span, bytes of the unit's rows copied
+  uint32_t issued = 0;           // stages filled so far
+  Span q;
 };
 
-// Fill the next stage (warp 0).  last_pass: the last pass whose units are
-// known.  Returns false when there is nothing (yet) to copy.
+// Fill stages through pass last_pass (whose units are known by now), until
+// `limit` stages have been filled in all.  Waits for a stage to be free.
 template <int WT>
-__device__ __forceinline__ bool few_issue(const Few<WT>& f, Cursor& c, int last_pass, int lane) {
-  while (c.u >= c.end) {
-    if (c.pass >= last_pass) return false;
-    ++c.pass;
-    const PassRange r = f.range(c.pass);
-    c.u = r.first;
-    c.end = r.last;
-    c.loaded = false;
-    c.off = 0;
+__device__ __forceinline__ void few_fill(const Few<WT>& f, Cursor& c, int last_pass, uint32_t limit, int lane) {
+  while (c.issued < limit) {
+    if (c.left == 0) {
+      while (c.u >= c.end) {
+        if (c.pass >= last_pass) return;
+        ++c.pass;
+        const PassRange r = f.range(c.pass);
+        c.u = r.first;
+        c.end = r.last;
+      }
+      c.q = f.span(c.pass, c.u, c.end);
+      c.left = c.q.units;
+      c.u += c.left;
+      c.off = 0;
+    }
+    const int slot = static_cast<int>(c.issued % kFewStages);
+    bool ok = true;
+    if (c.issued >= kFewStages) ok = mbar_wait(&f.s.empty[slot], (c.issued / kFewStages - 1) & 1u, &f.s.abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) return;
+    const int bytes = min(kFewChunk, c.q.len - c.off);
+    const int rows = c.q.step == 8 ? kFewRows : min(kFewRows, c.q.cols - c.q.col);
+    uint64_t* bar = &f.s.full[slot];
+    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(rows * bytes));
+    __syncwarp();
+    if (lane < rows) {
+      const char* src = c.q.w + (lane & 7) * c.q.row_bytes + (lane >> 3) * c.q.hi + c.off;
+      bulk_load(f.ring + slot * kFewStageBytes + lane * kFewPitch, src, static_cast<uint32_t>(bytes), bar);
+    }
+    ++c.issued;
+    c.off += bytes;
+    if (c.off >= c.q.len) {
+      --c.left;
+      c.off = 0;
+      c.q.col += c.q.step;
+      c.q.w += c.q.step * c.q.row_bytes;
+    }
   }
-  // one lane's reading decides for the warp
-  if (__shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&f.s.abort_flag), 0)) return false;
-  if (!c.loaded) {
-    c.cur = f.unit(c.pass, c.u);
-    c.loaded = true;
-  }
-  const int slot = static_cast<int>(c.issued % kFewStages);
-  const int bytes = min(kFewChunk, c.cur.len - c.off);
-  uint64_t* bar = &f.s.full[slot];
-  if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(c.cur.rows * bytes));
-  __syncwarp();
-  if (lane < c.cur.rows) {
-    const char* src = c.cur.w + (lane & 7) * c.cur.row_bytes + (lane >> 3) * c.cur.hi + c.off;
-    bulk_load(f.ring + slot * kFewStageBytes + lane * kFewPitch, src, static_cast<uint32_t>(bytes), bar);
-  }
-  ++c.issued;
-  c.off += bytes;
-  if (c.off >= c.cur.len) {
-    ++c.u;
-    c.loaded = false;
-    c.off = 0;
-  }
-  return true;
 }
 
 // One stage's products (cb bytes of each row): acc += weights x tokens.
@@ -333,6 +343,24 @@ struct FewMathMma {
     // (rows past the group's last repeat it: their sums are not read)
     const uint32_t ta = smem_addr(t) + min(lane & 7, n_tok - 1) * t_pitch + (lane >> 3) * 16;
     const uint32_t tb = smem_addr(t) + min(8 + (lane & 7), n_tok - 1) * t_pitch + (lane >> 3) * 16;
+    if (cb == kFewChunk && rows == kFewRows) {  // whole stage
+#pragma unroll
+      for (int i = 0; i < kFewChunk / 512; ++i) {
+        const int o = warp * 64 + i * 512;
+        uint32_t a0[4], a1[4], b[4];
+        ldmatrix_x4(wa + o, a0);
+        ldmatrix_x4(wa + o + 32, a1);
+        ldmatrix_x4(ta + o, b);
+        mma_16x8(acc[0], a0, b[0], b[1]);
+        mma_16x8(acc[0], a1, b[2], b[3]);
+        if (n_tok > 8) {
+          ldmatrix_x4(tb + o, b);
+          mma_16x8(acc[1], a0, b[0], b[1]);
+          mma_16x8(acc[1], a1, b[2], b[3]);
+        }
+      }
+      return;
+    }
     for (int o = warp * 64; o < cb; o += 8 * 64) {
       uint32_t a0[4], a1[4], b[4];
       ldmatrix_x4(wa + o, a0);
@@ -441,7 +469,7 @@ struct FewMath<kFewF32> {
 // Rows of the unit's group into the token buffer, zero behind the row's end up
 // to the next multiple of 64 bytes.  up: rows of x; down: a chunk of hidden rows.
 template <int WT>
-__device__ __forceinline__ void few_load_tokens(const Few<WT>& f, int pass, const Unit& q, int t_pitch, int tid) {
+__device__ __forceinline__ void few_load_tokens(const Few<WT>& f, int pass, const Span& q, int t_pitch, int tid) {
   const FewArgs& a = f.a;
   const bool up = pass <= kUpRouted;
   const bool routed = pass == kUpRouted || pass == kDownRouted;
@@ -511,7 +539,7 @@ __device__ __forceinline__ void few_load_tokens(const Few<WT>& f, int pass, cons
 
 // ------------------------------------------------------------- unit outputs
 template <int WT>
-__device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const Unit& q, const void* red, int tid) {
+__device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const Span& q, const void* red, int tid) {
   using M = FewMath<WT>;
   const FewArgs& a = f.a;
   if (pass <= kUpRouted) {  // 8 features x n tokens: lane groups of 8 share a token
@@ -545,7 +573,7 @@ __device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const
     }
   } else {  // 16 output channels x n tokens
     const int n = tid & 15, tok = tid >> 4;
-    if (tok < q.n && n < q.rows) {
+    if (tok < q.n && q.col + n < q.cols) {
       float v;
       if constexpr (WT == kFewI8) {
         const float sw = pass == kDownShared ? a.s2_s[q.col + n] : a.s2[static_cast<int64_t>(q.e) * a.d + q.col + n];
@@ -564,40 +592,40 @@ __device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const
 
 // All units of one pass that are this CTA's (the 256 worker threads).
 template <int WT>
-__device__ __forceinline__ void few_pass(const Few<WT>& f, int pass, Cursor& cur, uint32_t& used, uint8_t* red_base,
-                                         uint32_t& n_units, int last_pass, int tid) {
+__device__ __forceinline__ void few_pass(const Few<WT>& f, int pass, uint32_t& used, uint8_t* red_base,
+                                         uint32_t& n_units, int tid) {
   const int warp = tid >> 5, lane = tid & 31;
   const PassRange r = f.range(pass);
   FewMath<WT> math;
-  int held_e = -1, held_row = -1, held_c = -1;
-  for (int u = r.first; u < r.last; ++u) {
-    const Unit q = f.unit(pass, u);
+  for (int u = r.first; u < r.last;) {
+    Span q = f.span(pass, u, r.last);
+    u += q.units;
     const int t_pitch = ((q.len + 63) & ~63) + 16;
-    if (q.e != held_e || q.row0 != held_row || q.c != held_c) {
-      // the last unit's reads of the buffer (and of the row scales) are over
-      // only once its outputs are stored
-      named_bar_sync(1, kFewWorkers);
-      few_load_tokens(f, pass, q, t_pitch, tid);
-      held_e = q.e;
-      held_row = q.row0;
-      held_c = q.c;
-      named_bar_sync(1, kFewWorkers);
+    // the last unit's reads of the token buffer (and of the row scales) are
+    // over only once its outputs are stored
+    named_bar_sync(1, kFewWorkers);
+    few_load_tokens(f, pass, q, t_pitch, tid);
+    named_bar_sync(1, kFewWorkers);
+    for (int i = 0; i < q.units; ++i) {
+      math.clear();
+      uint8_t* red = red_base + (n_units & 1u) * (kFewRedBytes / 2);
+      const int rows = min(kFewRows, q.step == 8 ? kFewRows : q.cols - q.col);
+      for (int off = 0; off < q.len; off += kFewChunk) {
+        const int slot = static_cast<int>(used % kFewStages);
+        mbar_wait(&f.s.full[slot], (used / kFewStages) & 1u, &f.s.abort_flag);
+        __syncwarp();
+        math.stage(f.ring + slot * kFewStageBytes, f.tok + off, t_pitch, min(kFewChunk, q.len - off), q.n, rows, warp,
+                   lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&f.s.empty[slot]);
+        ++used;
+      }
+      math.put(red, q.n, warp, lane);
+      named_bar_sync(1, kFewWorkers);  // the unit's sums are complete
+      few_store_unit(f, pass, q, red, tid);
+      q.col += q.step;
+      ++n_units;  // the next unit's sums go to the other half: no barrier before they are written
     }
-    math.clear();
-    uint8_t* red = red_base + (n_units & 1u) * (kFewRedBytes / 2);
-    for (int off = 0; off < q.len; off += kFewChunk) {
-      const int slot = static_cast<int>(used % kFewStages);
-      mbar_wait(&f.s.full[slot], (used / kFewStages) & 1u, &f.s.abort_flag);
-      __syncwarp();
-      math.stage(f.ring + slot * kFewStageBytes, f.tok + off, t_pitch, min(kFewChunk, q.len - off), q.n, q.rows, warp,
-                 lane);
-      if (off + kFewChunk >= q.len) math.put(red, q.n, warp, lane);
-      ++used;
-      named_bar_sync(1, kFewWorkers);  // the stage is free, the sums are complete
-      if (warp == 0) few_issue(f, cur, last_pass, lane);
-    }
-    few_store_unit(f, pass, q, red, tid);
-    ++n_units;  // the next unit's sums go to the other half: no barrier before they are written
   }
 }
 
@@ -763,8 +791,8 @@ __device__ __forceinline__ void few_dispatch(const FewArgs& a, FewShared& s, con
   }
 }
 
-// s.groups: prefix of ceil(kept / ng) over the experts (one warp)
-__device__ __forceinline__ void few_groups(const FewArgs& a, FewShared& s, int ng, int lane) {
+// groups: prefix of ceil(kept / ng) over the experts (one warp)
+__device__ __forceinline__ void few_groups(const FewArgs& a, const FewShared& s, int* groups, int ng, int lane) {
   int g[kMaxExperts / 32], sum = 0;
 #pragma unroll
   for (int i = 0; i < kMaxExperts / 32; ++i) {
@@ -782,10 +810,10 @@ __device__ __forceinline__ void few_groups(const FewArgs& a, FewShared& s, int n
 #pragma unroll
   for (int i = 0; i < kMaxExperts / 32; ++i) {
     const int e = lane * (kMaxExperts / 32) + i;
-    if (e <= a.E) s.groups[e] = run;
+    if (e <= a.E) groups[e] = run;
     run += g[i];
   }
-  if (lane == 31 && a.E == kMaxExperts) s.groups[kMaxExperts] = run;
+  if (lane == 31 && a.E == kMaxExperts) groups[kMaxExperts] = run;
 }
 
 // y_t = sum over the shared experts' chunks + sum_k w_k (sum of Expert_k's chunks)
@@ -833,10 +861,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   FewShared& s = *reinterpret_cast<FewShared*>(red + kFewRedBytes);
   cg::grid_group grid = cg::this_grid();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool worker = warp < kFewWorkers / 32;
+  const bool worker = warp < kFewWorkers / 32, copier = warp == kFewWorkers / 32;
 
   if (tid == 0) {
-    for (int i = 0; i < kFewStages; ++i) mbar_init(&s.full[i], 1);
+    for (int i = 0; i < kFewStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], kFewWorkers / 32);
+    }
     s.abort_flag = 0;
     fence_barrier_init();
   }
@@ -851,15 +882,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   }
   __syncthreads();
 
-  Few<WT> f(a, s, ring, tok);
+  const Few<WT> f(a, s, ring, tok);
   Cursor cur;
   uint32_t used = 0, n_units = 0;
-  if (warp == 0) {  // the shared experts' weights do not wait for the routing
+  if (copier) {  // the shared experts' weights do not wait for the routing
     const PassRange r = f.range(kUpShared);
     cur.u = r.first;
     cur.end = r.last;
-    for (int i = 0; i < kFewStages; ++i)
-      if (!few_issue(f, cur, kUpShared, lane)) break;
+    few_fill(f, cur, kUpShared, kFewStages, lane);
   }
   if (worker && !a.given) few_logits<X>(a, reinterpret_cast<double*>(red), tid);
   grid.sync();
@@ -879,15 +909,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
       few_select<8>(a, s, idx, w, with_stats, tid);
     named_bar_sync(1, kFewWorkers);
     few_dispatch(a, s, idx, w, write, tid);
-    if (warp == 0) few_groups(a, s, a.ng_up, lane);
+    if (warp < 2) few_groups(a, s, s.groups[warp], warp == 0 ? a.ng_up : a.ng_down, lane);
   }
   __syncthreads();
   if (worker) {
-    if (warp == 0)
-      while (cur.issued < kFewStages && few_issue(f, cur, kUpRouted, lane)) {
-      }
-    few_pass(f, kUpShared, cur, used, red, n_units, kUpRouted, tid);
-    few_pass(f, kUpRouted, cur, used, red, n_units, kUpRouted, tid);
+    few_pass(f, kUpShared, used, red, n_units, tid);
+    few_pass(f, kUpRouted, used, red, n_units, tid);
+  } else if (copier) {
+    few_fill(f, cur, kUpRouted, 0xffffffffu, lane);
+    // the first stages of the down products, as the last of the up products are
+    // consumed: those copies run while the CTA waits for the others
+    few_fill(f, cur, kDownRouted, cur.issued + kFewStages, lane);
   } else if (blockIdx.x == 0 && a.stats) {
     // the statistics, beside the other warps' work
     for (int e = lane; e < a.E; e += 32)
@@ -903,27 +935,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
       }
     }
   }
-  __syncthreads();
-  if (warp == 0) {  // the down products' groups; their first weights before the barrier
-    if (a.ng_down != a.ng_up) few_groups(a, s, a.ng_down, lane);
-    __syncwarp();
-    while (cur.issued < used + kFewStages && few_issue(f, cur, kDownRouted, lane)) {
-    }
-  }
   grid.sync();
   if (worker) {
-    few_pass(f, kDownShared, cur, used, red, n_units, kDownRouted, tid);
-    few_pass(f, kDownRouted, cur, used, red, n_units, kDownRouted, tid);
+    few_pass(f, kDownShared, used, red, n_units, tid);
+    few_pass(f, kDownRouted, used, red, n_units, tid);
+  } else if (copier) {
+    few_fill(f, cur, kDownRouted, 0xffffffffu, lane);
   }
   grid.sync();
   if (worker) few_combine<X>(a, tid);
-  if (warp == 0 && s.abort_flag) {  // gave up a wait: let every copy land before the block ends
-    if (lane == 0) {
-      int never = 0;
-      for (uint32_t i = cur.issued > kFewStages ? cur.issued - kFewStages : 0; i < cur.issued; ++i)
-        mbar_wait(&s.full[i % kFewStages], (i / kFewStages) & 1u, &never);
-      raise_status(a.status, kDevWaitTimeout);
-    }
+  if (copier && lane == 0 && *static_cast<volatile int*>(&s.abort_flag)) {
+    // gave up a wait: let every copy land before the block ends
+    int never = 0;
+    for (uint32_t i = cur.issued > kFewStages ? cur.issued - kFewStages : 0; i < cur.issued; ++i)
+      mbar_wait(&s.full[i % kFewStages], (i / kFewStages) & 1u, &never);
+    raise_status(a.status, kDevWaitTimeout);
   }
 }
 
