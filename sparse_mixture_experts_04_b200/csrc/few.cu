@@ -7,8 +7,9 @@
 // of six launches:
 //
 //   1. logits    tiles of 4 experts x 4 tokens over the CTAs        grid barrier
-//   2. routing   every CTA ranks all tokens itself (softmax, top-K, capacity,
-//                slots), so no barrier follows; CTA 0 writes the outputs
+//   2. routing   softmax and top-K: up to 8 tokens every CTA for itself, more
+//                of them one token per CTA                          grid barrier
+//                capacity and slots: every CTA for itself; CTA 0 writes them
 //   3. up        h = silu(W_gate x) * (W_up x)                      grid barrier
 //   4. down      partial sums of W_down h, FP32                     grid barrier
 //   5. combine   y_t = sum of the shared experts + sum_k w_k Expert_k(x_t)
@@ -60,14 +61,14 @@ constexpr int kFewStages = 4;
 constexpr int kFewStageBytes = kFewRows * kFewPitch;
 constexpr int kFewTokBytes = 69632;              // the unit's tokens (8 rows of 8 KB)
 constexpr int kFewMaxPairs = kFewMaxTokens * kMaxTopK;
-constexpr int kFewRedBytes = 2 * 8 * 2 * 128 * 4;  // [2][8 warps][2 token tiles][16 x 8] sums
+constexpr int kFewRedBytes = 2 * 8 * 2 * 128 * 4;  // [teams][2][8 / teams warps][2 token tiles][16 x 8] sums
 
 struct FewShared {
   uint64_t full[kFewStages];
   uint64_t empty[kFewStages];
   unsigned long long mask[kMaxExperts];   // tokens that chose the expert
-  unsigned long long psum[kMaxExperts];   // sum of p, fixed point; then f_e P_e as doubles (statistics)
-  double zsum[8];
+  double fp[kMaxExperts];                 // f_e P_e (statistics)
+  unsigned long long scan[8];             // warp totals of few_dispatch's prefix sums
   int counts[kMaxExperts];
   int kept[kMaxExperts];
   int seg_off[kMaxExperts + 1];
@@ -112,11 +113,15 @@ struct FewArgs {
   float* part;         // [nc][T K][d] partial sums by slot
   float* part_s;       // [N_s nc][T][d]
   unsigned* status;
+  unsigned* arrivals;          // [3] CTAs that reached each grid barrier (cleared before the first)
+  unsigned long long* psum;    // [E] sum of p, fixed point (statistics; cleared likewise)
+  float* lse2;                 // [T] squared logsumexp of each token (statistics)
   int T, d, E, K, Ns, F;
   long long cap;       // -1: no limit
   int given, bias_on_logit, extended;
   float alpha;
   double pscale;
+  int spread;          // top-K: one token per CTA instead of every CTA all tokens
   // tiling (host): token rows per group, reduction chunks of the down product
   int ng_up, ng_down, nc, chunk_bytes;
 };
@@ -152,6 +157,29 @@ __device__ __forceinline__ void mma_16x8(int (&c)[4], const uint32_t (&a)[4], ui
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Grid barrier of the worker threads: the CTA's writes before it are seen by
+// every CTA's reads (past L1) after it.  All CTAs are resident and every one
+// of them arrives whatever its copies do; the wait is bounded all the same.
+__device__ __forceinline__ void few_grid_sync(unsigned* arrivals, int* abort_flag, int tid) {
+  named_bar_sync(1, kFewWorkers);
+  if (tid == 0) {
+    __threadfence();
+    atomicAdd(arrivals, 1u);
+    const unsigned long long t0 = global_ns();
+    unsigned n;
+    for (unsigned i = 1;; ++i) {
+      asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(n) : "l"(arrivals) : "memory");
+      if (n >= gridDim.x) break;
+      if ((i & 255u) == 0 && global_ns() - t0 > kWaitLimitNs) {
+        *reinterpret_cast<volatile int*>(abort_flag) = 1;
+        break;
+      }
+    }
+    __threadfence();
+  }
+  named_bar_sync(1, kFewWorkers);
+}
+
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
 
 // The four passes over weights: shared and routed experts, up and down.
@@ -179,7 +207,10 @@ struct Span {
 template <int WT>
 struct Few {
   static constexpr int kW = WT == kFewF32 ? 4 : WT == kFewBF16 ? 2 : 1;  // bytes of a weight
-  static constexpr int kTiles = WT == kFewF32 ? 1 : 2;                   // 8-token tiles of a group
+  // The worker warps work as teams, each on its own unit: while one adds up its
+  // warps' sums and stores them, the other multiplies.
+  static constexpr int kTeams = WT == kFewF32 ? 1 : 2;
+  static constexpr int kTeamWarps = kFewWorkers / 32 / kTeams;
   using Acc = typename std::conditional<WT == kFewI8, int, float>::type;
 
   const FewArgs& a;
@@ -269,20 +300,25 @@ struct Few {
   }
 };
 
-// The copy side of the ring (one warp, every lane alike): the stages are
-// filled in the order in which they are consumed.
+// The copy side (one warp, every lane alike).  Each team has its own ring of
+// kFewStages / teams stages, so that a team never waits for a phase of a barrier
+// more than one ahead (a parity wait could not tell it from the past one).  The
+// teams' units of a span are copied together, a stage of each in turn: stage k
+// of units i, i + 1, then stage k + 1 of both.
 struct Cursor {
   int pass = 0, u = 0, end = 0;  // next unit of the pass, the pass's last
-  int left = 0, off = 0;         // units left in the span, bytes of the unit's rows copied
-  uint32_t issued = 0;           // stages filled so far
+  int left = 0, off = 0;         // units left in the span, bytes of the current units' rows copied
+  int team = 0;                  // team whose stage is next
+  uint32_t issued0 = 0, issued1 = 0;  // stages filled so far, by team
   Span q;
 };
 
-// Fill stages through pass last_pass (whose units are known by now), until
-// `limit` stages have been filled in all.  Waits for a stage to be free.
+// Fill stages through pass last_pass (whose units are known by now); before the
+// routing (kUpShared) only the stages that are free, afterwards waiting for each.
 template <int WT>
-__device__ __forceinline__ void few_fill(const Few<WT>& f, Cursor& c, int last_pass, uint32_t limit, int lane) {
-  while (c.issued < limit) {
+__device__ __forceinline__ void few_fill(const Few<WT>& f, Cursor& c, int last_pass, int lane) {
+  constexpr int kTeams = Few<WT>::kTeams, kSlots = kFewStages / kTeams;
+  for (;;) {
     if (c.left == 0) {
       while (c.u >= c.end) {
         if (c.pass >= last_pass) return;
@@ -295,27 +331,38 @@ __device__ __forceinline__ void few_fill(const Few<WT>& f, Cursor& c, int last_p
       c.left = c.q.units;
       c.u += c.left;
       c.off = 0;
+      c.team = 0;
     }
-    const int slot = static_cast<int>(c.issued % kFewStages);
+    const uint32_t issued = c.team ? c.issued1 : c.issued0;
+    if (last_pass == kUpShared && issued >= kSlots) return;
+    const int slot = c.team * kSlots + static_cast<int>(issued % kSlots);
     bool ok = true;
-    if (c.issued >= kFewStages) ok = mbar_wait(&f.s.empty[slot], (c.issued / kFewStages - 1) & 1u, &f.s.abort_flag);
+    if (issued >= kSlots) ok = mbar_wait(&f.s.empty[slot], (issued / kSlots - 1) & 1u, &f.s.abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return;
     const int bytes = min(kFewChunk, c.q.len - c.off);
-    const int rows = c.q.step == 8 ? kFewRows : min(kFewRows, c.q.cols - c.q.col);
+    const int col = c.q.col + c.team * c.q.step;
+    const int rows = c.q.step == 8 ? kFewRows : min(kFewRows, c.q.cols - col);
     uint64_t* bar = &f.s.full[slot];
     if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(rows * bytes));
     __syncwarp();
     if (lane < rows) {
-      const char* src = c.q.w + (lane & 7) * c.q.row_bytes + (lane >> 3) * c.q.hi + c.off;
+      const char* src = c.q.w + (c.team * c.q.step + (lane & 7)) * c.q.row_bytes + (lane >> 3) * c.q.hi + c.off;
       bulk_load(f.ring + slot * kFewStageBytes + lane * kFewPitch, src, static_cast<uint32_t>(bytes), bar);
     }
-    ++c.issued;
-    c.off += bytes;
-    if (c.off >= c.q.len) {
-      --c.left;
-      c.off = 0;
-      c.q.col += c.q.step;
-      c.q.w += c.q.step * c.q.row_bytes;
+    if (c.team)
+      ++c.issued1;
+    else
+      ++c.issued0;
+    const int now = min(kTeams, c.left);  // units copied together
+    if (++c.team >= now) {
+      c.team = 0;
+      c.off += bytes;
+      if (c.off >= c.q.len) {
+        c.left -= now;
+        c.off = 0;
+        c.q.col += now * c.q.step;
+        c.q.w += now * c.q.step * c.q.row_bytes;
+      }
     }
   }
 }
@@ -324,9 +371,11 @@ __device__ __forceinline__ void few_fill(const Few<WT>& f, Cursor& c, int last_p
 template <int WT>
 struct FewMath;
 
+// warp: the warp's place in its team.
 template <int WT>
 struct FewMathMma {
   using Acc = typename Few<WT>::Acc;
+  static constexpr int kWarps = Few<WT>::kTeamWarps;
   Acc acc[2][4];
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -345,8 +394,8 @@ struct FewMathMma {
     const uint32_t tb = smem_addr(t) + min(8 + (lane & 7), n_tok - 1) * t_pitch + (lane >> 3) * 16;
     if (cb == kFewChunk && rows == kFewRows) {  // whole stage
 #pragma unroll
-      for (int i = 0; i < kFewChunk / 512; ++i) {
-        const int o = warp * 64 + i * 512;
+      for (int i = 0; i < kFewChunk / (64 * kWarps); ++i) {
+        const int o = (i * kWarps + warp) * 64;
         uint32_t a0[4], a1[4], b[4];
         ldmatrix_x4(wa + o, a0);
         ldmatrix_x4(wa + o + 32, a1);
@@ -361,7 +410,7 @@ struct FewMathMma {
       }
       return;
     }
-    for (int o = warp * 64; o < cb; o += 8 * 64) {
+    for (int o = warp * 64; o < cb; o += kWarps * 64) {
       uint32_t a0[4], a1[4], b[4];
       ldmatrix_x4(wa + o, a0);
       ldmatrix_x4(wa + o + 32, a1);
@@ -397,7 +446,7 @@ struct FewMathMma {
     const Acc* r = static_cast<const Acc*>(red) + (tok >> 3) * 128 + row * 8 + (tok & 7);
     Acc v = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) v += r[w * 256];
+    for (int w = 0; w < kWarps; ++w) v += r[w * 256];
     return v;
   }
 };
@@ -572,15 +621,17 @@ __device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const
         atomicMax(a.amax + (pass == kUpShared ? static_cast<int64_t>(a.T) * a.K : 0) + q.row0 + tok, m);
     }
   } else {  // 16 output channels x n tokens
-    const int n = tid & 15, tok = tid >> 4;
-    if (tok < q.n && q.col + n < q.cols) {
+    const int n = tid & 15;
+    if (q.col + n >= q.cols) return;
+    float sw = 0.f;
+    if constexpr (WT == kFewI8)
+      sw = pass == kDownShared ? a.s2_s[q.col + n] : a.s2[static_cast<int64_t>(q.e) * a.d + q.col + n];
+    for (int tok = tid >> 4; tok < q.n; tok += Few<WT>::kTeamWarps * 2) {
       float v;
-      if constexpr (WT == kFewI8) {
-        const float sw = pass == kDownShared ? a.s2_s[q.col + n] : a.s2[static_cast<int64_t>(q.e) * a.d + q.col + n];
+      if constexpr (WT == kFewI8)
         v = __int2float_rn(M::get(red, n, tok)) * (f.s.row_scale[tok] * sw);
-      } else {
+      else
         v = M::get(red, n, tok);
-      }
       const int64_t row = q.row0 + tok;
       if (pass == kDownShared)
         a.part_s[((static_cast<int64_t>(q.e) * a.nc + q.c) * a.T + row) * a.d + q.col + n] = v;
@@ -590,13 +641,16 @@ __device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const
   }
 }
 
-// All units of one pass that are this CTA's (the 256 worker threads).
+// All units of one pass that are this CTA's (the 256 worker threads).  Team t
+// takes units t, t + teams, ... of a span; `used`: stages this team has consumed.
 template <int WT>
 __device__ __forceinline__ void few_pass(const Few<WT>& f, int pass, uint32_t& used, uint8_t* red_base,
                                          uint32_t& n_units, int tid) {
-  const int warp = tid >> 5, lane = tid & 31;
+  constexpr int kTeams = Few<WT>::kTeams, kWarps = Few<WT>::kTeamWarps, kSlots = kFewStages / kTeams;
+  const int lane = tid & 31, team = (tid >> 5) / kWarps, warp = (tid >> 5) % kWarps;
   const PassRange r = f.range(pass);
   FewMath<WT> math;
+  red_base += team * (kFewRedBytes / kTeams);
   for (int u = r.first; u < r.last;) {
     Span q = f.span(pass, u, r.last);
     u += q.units;
@@ -606,24 +660,24 @@ __device__ __forceinline__ void few_pass(const Few<WT>& f, int pass, uint32_t& u
     named_bar_sync(1, kFewWorkers);
     few_load_tokens(f, pass, q, t_pitch, tid);
     named_bar_sync(1, kFewWorkers);
-    for (int i = 0; i < q.units; ++i) {
+    q.col += team * q.step;
+    for (int i = team; i < q.units; i += kTeams) {
       math.clear();
-      uint8_t* red = red_base + (n_units & 1u) * (kFewRedBytes / 2);
+      uint8_t* red = red_base + (n_units & 1u) * (kFewRedBytes / kTeams / 2);
       const int rows = min(kFewRows, q.step == 8 ? kFewRows : q.cols - q.col);
-      for (int off = 0; off < q.len; off += kFewChunk) {
-        const int slot = static_cast<int>(used % kFewStages);
-        mbar_wait(&f.s.full[slot], (used / kFewStages) & 1u, &f.s.abort_flag);
+      for (int off = 0; off < q.len; off += kFewChunk, ++used) {
+        const int slot = team * kSlots + static_cast<int>(used % kSlots);
+        mbar_wait(&f.s.full[slot], (used / kSlots) & 1u, &f.s.abort_flag);
         __syncwarp();
         math.stage(f.ring + slot * kFewStageBytes, f.tok + off, t_pitch, min(kFewChunk, q.len - off), q.n, rows, warp,
                    lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&f.s.empty[slot]);
-        ++used;
       }
       math.put(red, q.n, warp, lane);
-      named_bar_sync(1, kFewWorkers);  // the unit's sums are complete
-      few_store_unit(f, pass, q, red, tid);
-      q.col += q.step;
+      named_bar_sync(2 + team, kWarps * 32);  // the unit's sums are complete
+      few_store_unit(f, pass, q, red, tid - team * kWarps * 32);
+      q.col += kTeams * q.step;
       ++n_units;  // the next unit's sums go to the other half: no barrier before they are written
     }
   }
@@ -688,159 +742,186 @@ __device__ __forceinline__ void few_logits(const FewArgs& a, double* red, int ti
   }
 }
 
-// Softmax and top-K of every token (each warp its own), into idx / w [T K].
+// Softmax and top-K of tokens first, first + step, ... (one warp), into idx / w
+// [T K]; stats: also the sums of p and the squared logsumexp.
 template <int EPL>
 __device__ __forceinline__ void few_select(const FewArgs& a, FewShared& s, int32_t* idx, float* w, bool with_stats,
-                                           int tid) {
-  const int warp = tid >> 5, lane = tid & 31;
+                                           int first, int step, int lane) {
   float bias[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + 32 * i;
     bias[i] = (a.sel_bias && e < a.E) ? a.sel_bias[e] : 0.f;
   }
-  float zacc = 0.f;
-  double zsum = 0.0;
-  for (int t = warp; t < a.T; t += kFewWorkers / 32) {
-    float lg[EPL], p[EPL];
+#pragma unroll 1
+  for (int t = first; t < a.T; t += step) {
+    float lg[EPL], p[EPL], zacc = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const int e = lane + 32 * i;
       lg[i] = e < a.E ? __ldcg(a.logits + static_cast<int64_t>(t) * a.E + e) : -INFINITY;
       p[i] = 0.f;
     }
-    zacc = 0.f;
     select_token_group<EPL, 32>(lg, bias, a.sel_bias != nullptr, a.bias_on_logit, a.E, a.K, lane, p, zacc,
                                 idx + t * a.K, w + t * a.K, s.counts);
-    zsum += static_cast<double>(zacc);
     if (with_stats) {
+      if (lane == 0) a.lse2[t] = zacc;
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
         if (lane + 32 * i < a.E && p[i] > 0.f)
-          atomicAdd(&s.psum[lane + 32 * i], __double2ull_rn(static_cast<double>(p[i]) * a.pscale));
+          atomicAdd(a.psum + lane + 32 * i, __double2ull_rn(static_cast<double>(p[i]) * a.pscale));
     }
   }
-  if (lane == 0) s.zsum[warp] = zsum;
+}
+
+__device__ __forceinline__ void few_select_any(const FewArgs& a, FewShared& s, int32_t* idx, float* w,
+                                               bool with_stats, int first, int step, int lane) {
+  if (a.E <= 32)
+    few_select<1>(a, s, idx, w, with_stats, first, step, lane);
+  else if (a.E <= 64)
+    few_select<2>(a, s, idx, w, with_stats, first, step, lane);
+  else if (a.E <= 128)
+    few_select<4>(a, s, idx, w, with_stats, first, step, lane);
+  else
+    few_select<8>(a, s, idx, w, with_stats, first, step, lane);
 }
 
 // Capacity, slots and the experts' token groups from idx (the 256 workers).
+// The token's rank within its expert is the number of earlier tokens in the
+// expert's bit mask.  (Written with few instructions: the code runs once, and
+// fetching it costs more than executing it.)
 __device__ __forceinline__ void few_dispatch(const FewArgs& a, FewShared& s, const int32_t* idx, const float* w,
                                              bool write, int tid) {
-  const int TK = a.T * a.K;
+  static_assert(kMaxExperts == kFewWorkers, "one worker thread per expert");
+  const int TK = a.T * a.K, lane = tid & 31;
+#pragma unroll 1
   for (int i = tid; i < TK; i += kFewWorkers) {
-    const int e = idx[i];
-    if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicOr(&s.mask[e], 1ull << (i / a.K));
+    const unsigned e = static_cast<unsigned>(idx[i]), t = static_cast<unsigned>(i) / a.K;
+    // 32-bit halves: a native shared-memory atomic
+    if (e < static_cast<unsigned>(a.E)) atomicOr(reinterpret_cast<unsigned*>(&s.mask[e]) + (t >> 5), 1u << (t & 31));
   }
   named_bar_sync(1, kFewWorkers);
+  // thread e: the expert's rows and token groups; one scan over the experts of
+  // the three counts, 20 bits each (at most 2048 rows in all)
+  const int n = __popcll(s.mask[tid]);
+  int k = 0;
   if (tid < a.E) {
-    const int n = __popcll(s.mask[tid]);
     long long cap = a.cap;
     if (a.expert_cap) cap = a.expert_cap[tid];
-    const int k = (cap < 0 || n < cap) ? n : static_cast<int>(cap);
+    k = (cap < 0 || n < cap) ? n : static_cast<int>(cap);
     s.kept[tid] = k;
-    if (write) {
-      a.counts[tid] = n;
-      a.kept[tid] = k;
-    }
+    s.counts[tid] = n;
+  }
+  const unsigned long long mine = static_cast<unsigned long long>(k) |
+                                  static_cast<unsigned long long>((k + a.ng_up - 1) / a.ng_up) << 20 |
+                                  static_cast<unsigned long long>((k + a.ng_down - 1) / a.ng_down) << 40;
+  unsigned long long incl = mine;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s.scan[tid >> 5] = incl;
+  named_bar_sync(1, kFewWorkers);
+#pragma unroll 1
+  for (int i = 0; i < (tid >> 5); ++i) incl += s.scan[i];
+  const unsigned long long excl = incl - mine;
+  const int off = static_cast<int>(excl & 0xFFFFFu);
+  s.seg_off[tid] = off;
+  s.groups[0][tid] = static_cast<int>((excl >> 20) & 0xFFFFFu);
+  s.groups[1][tid] = static_cast<int>(excl >> 40);
+  // (an expert past the last has no rows, so entry E is the total)
+  if (tid == kMaxExperts - 1) {
+    s.seg_off[kMaxExperts] = static_cast<int>(incl & 0xFFFFFu);
+    s.groups[0][kMaxExperts] = static_cast<int>((incl >> 20) & 0xFFFFFu);
+    s.groups[1][kMaxExperts] = static_cast<int>(incl >> 40);
+  }
+  if (write && tid < a.E) {
+    a.counts[tid] = n;
+    a.kept[tid] = k;
+    a.seg_off[tid] = off;
+    if (tid == a.E - 1) a.seg_off[a.E] = off + k;
   }
   named_bar_sync(1, kFewWorkers);
-  if (tid < 32) {  // exclusive prefix over the experts, 8 per lane
-    int k[kMaxExperts / 32], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) {
-      const int e = tid * (kMaxExperts / 32) + i;
-      k[i] = e < a.E ? s.kept[e] : 0;
-      sum += k[i];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (tid >= o) incl += v;
-    }
-    int run = incl - sum;
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) {
-      const int e = tid * (kMaxExperts / 32) + i;
-      if (e <= a.E) {
-        s.seg_off[e] = run;
-        if (write) a.seg_off[e] = run;
-      }
-      run += k[i];
-    }
-    if (tid == 31 && a.E == kMaxExperts) {
-      s.seg_off[kMaxExperts] = run;
-      if (write) a.seg_off[kMaxExperts] = run;
-    }
-  }
-  named_bar_sync(1, kFewWorkers);
+#pragma unroll 1
   for (int i = tid; i < TK; i += kFewWorkers) {
-    const int e = idx[i], t = i / a.K;
+    const unsigned e = static_cast<unsigned>(idx[i]), t = static_cast<unsigned>(i) / a.K;
     int slot = -1;
-    if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) {
-      const int rank = __popcll(s.mask[e] & ((1ull << t) - 1ull));  // earlier tokens of the same expert
+    if (e < static_cast<unsigned>(a.E)) {
+      const int rank = __popcll(s.mask[e] & ((1ull << t) - 1ull));
       if (rank < s.kept[e]) slot = s.seg_off[e] + rank;
     }
     if (slot >= 0) s.perm[slot] = static_cast<uint16_t>(i);
     if (write) {
-      a.topk_idx[i] = e;
-      a.topk_w[i] = w[i];
       a.slot_of[i] = slot;
       if (slot >= 0) a.perm[slot] = i;
+      if (w) {
+        a.topk_idx[i] = static_cast<int>(e);
+        a.topk_w[i] = w[i];
+      }
     }
   }
 }
 
-// groups: prefix of ceil(kept / ng) over the experts (one warp)
-__device__ __forceinline__ void few_groups(const FewArgs& a, const FewShared& s, int* groups, int ng, int lane) {
-  int g[kMaxExperts / 32], sum = 0;
-#pragma unroll
-  for (int i = 0; i < kMaxExperts / 32; ++i) {
-    const int e = lane * (kMaxExperts / 32) + i;
-    g[i] = e < a.E ? (s.kept[e] + ng - 1) / ng : 0;
-    sum += g[i];
-  }
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  int run = incl - sum;
-#pragma unroll
-  for (int i = 0; i < kMaxExperts / 32; ++i) {
-    const int e = lane * (kMaxExperts / 32) + i;
-    if (e <= a.E) groups[e] = run;
-    run += g[i];
-  }
-  if (lane == 31 && a.E == kMaxExperts) groups[kMaxExperts] = run;
-}
-
-// y_t = sum over the shared experts' chunks + sum_k w_k (sum of Expert_k's chunks)
+// y_t = sum over the shared experts' chunks + sum_k w_k (sum of Expert_k's
+// chunks), k ascending; the loads of four addends at a time are in flight.
 template <typename T>
 __device__ __forceinline__ void few_combine(const FewArgs& a, int tid) {
   const int vecs = a.d / 4;
-  const int64_t total = static_cast<int64_t>(a.T) * vecs;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kFewWorkers + tid; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kFewWorkers) {
-    const int t = static_cast<int>(i / vecs), c = static_cast<int>(i - static_cast<int64_t>(t) * vecs) * 4;
+  const int total = a.T * vecs;
+#pragma unroll 1
+  for (int i = blockIdx.x * kFewWorkers + tid; i < total; i += gridDim.x * kFewWorkers) {
+    const int t = i / vecs, c = (i - t * vecs) * 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int n = 0; n < a.Ns * a.nc; ++n) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_s + (static_cast<int64_t>(n) * a.T + t) * a.d + c));
-      acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
-    }
-    for (int k = 0; k < a.K; ++k) {
-      const int slot = __ldcg(a.slot_of + t * a.K + k);
-      if (slot < 0) continue;
-      const float w = __ldcg(a.topk_w + t * a.K + k);
-      float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int n = 0; n < a.nc; ++n) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(
-            a.part + (static_cast<int64_t>(n) * a.T * a.K + slot) * a.d + c));
-        e.x += v.x; e.y += v.y; e.z += v.z; e.w += v.w;
+    const int ns = a.Ns * a.nc, nr = a.K * a.nc;
+#pragma unroll 1
+    for (int n0 = 0; n0 < ns; n0 += 4) {
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (n0 + j < ns)
+          v[j] = __ldcg(reinterpret_cast<const float4*>(a.part_s + (static_cast<int64_t>(n0 + j) * a.T + t) * a.d + c));
       }
-      acc.x = fmaf(w, e.x, acc.x); acc.y = fmaf(w, e.y, acc.y);
-      acc.z = fmaf(w, e.z, acc.z); acc.w = fmaf(w, e.w, acc.w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc.x += v[j].x; acc.y += v[j].y; acc.z += v[j].z; acc.w += v[j].w;
+      }
+    }
+    float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
+    int n = 0, k = 0;  // next addend: chunk n of the k-th choice
+#pragma unroll 1
+    for (int m0 = 0; m0 < nr; m0 += 4) {
+      float4 v[4];
+      float w[4];
+      bool last[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        w[j] = 0.f;
+        last[j] = false;
+        if (m0 + j < nr) {
+          const int slot = __ldcg(a.slot_of + t * a.K + k);
+          if (slot >= 0) {
+            v[j] = __ldcg(reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(n) * a.T * a.K + slot) * a.d + c));
+            w[j] = __ldcg(a.topk_w + t * a.K + k);
+          }
+          last[j] = slot >= 0 && n + 1 == a.nc;
+          if (++n == a.nc) {
+            n = 0;
+            ++k;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        e.x += v[j].x; e.y += v[j].y; e.z += v[j].z; e.w += v[j].w;
+        if (last[j]) {
+          acc.x = fmaf(w[j], e.x, acc.x); acc.y = fmaf(w[j], e.y, acc.y);
+          acc.z = fmaf(w[j], e.z, acc.z); acc.w = fmaf(w[j], e.w, acc.w);
+          e = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
     }
     T* yp = static_cast<T*>(a.y) + static_cast<int64_t>(t) * a.d + c;
     if constexpr (sizeof(T) == 2)
@@ -866,16 +947,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   if (tid == 0) {
     for (int i = 0; i < kFewStages; ++i) {
       mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], kFewWorkers / 32);
+      mbar_init(&s.empty[i], Few<WT>::kTeamWarps);
     }
     s.abort_flag = 0;
     fence_barrier_init();
   }
   for (int i = tid; i < kMaxExperts; i += kFewThreads) {
     s.mask[i] = 0;
-    s.psum[i] = 0;
-    s.counts[i] = 0;
+    if (blockIdx.x == 0 && i < a.E) a.psum[i] = 0;
   }
+  if (blockIdx.x == 0 && tid < 3) a.arrivals[tid] = 0;
   if (blockIdx.x == 0 && tid == 0) *a.status = 0;
   if (WT == kFewI8) {
     for (int i = blockIdx.x * kFewThreads + tid; i < a.T * a.K + a.T; i += gridDim.x * kFewThreads) a.amax[i] = 0;
@@ -889,68 +970,66 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     const PassRange r = f.range(kUpShared);
     cur.u = r.first;
     cur.end = r.last;
-    few_fill(f, cur, kUpShared, kFewStages, lane);
+    few_fill(f, cur, kUpShared, lane);
   }
   if (worker && !a.given) few_logits<X>(a, reinterpret_cast<double*>(red), tid);
   grid.sync();
 
   if (worker) {
     int32_t* idx = reinterpret_cast<int32_t*>(tok);
-    float* w = reinterpret_cast<float*>(tok) + kFewMaxPairs;
     const bool write = blockIdx.x == 0;
-    const bool with_stats = write && a.stats;
-    if (a.E <= 32)
-      few_select<1>(a, s, idx, w, with_stats, tid);
-    else if (a.E <= 64)
-      few_select<2>(a, s, idx, w, with_stats, tid);
-    else if (a.E <= 128)
-      few_select<4>(a, s, idx, w, with_stats, tid);
-    else
-      few_select<8>(a, s, idx, w, with_stats, tid);
-    named_bar_sync(1, kFewWorkers);
-    few_dispatch(a, s, idx, w, write, tid);
-    if (warp < 2) few_groups(a, s, s.groups[warp], warp == 0 ? a.ng_up : a.ng_down, lane);
+    if (a.spread) {
+      few_select_any(a, s, a.topk_idx, a.topk_w, a.stats != nullptr, blockIdx.x + warp * gridDim.x,
+                     gridDim.x * (kFewWorkers / 32), lane);
+      few_grid_sync(a.arrivals, &s.abort_flag, tid);
+#pragma unroll 1
+      for (int i = tid; i < a.T * a.K; i += kFewWorkers) idx[i] = __ldcg(a.topk_idx + i);
+      named_bar_sync(1, kFewWorkers);
+      few_dispatch(a, s, idx, nullptr, write, tid);
+    } else {
+      float* w = reinterpret_cast<float*>(tok) + kFewMaxPairs;
+      few_select_any(a, s, idx, w, write && a.stats, warp, kFewWorkers / 32, lane);
+      named_bar_sync(1, kFewWorkers);
+      few_dispatch(a, s, idx, w, write, tid);
+    }
   }
   __syncthreads();
   if (worker) {
     few_pass(f, kUpShared, used, red, n_units, tid);
     few_pass(f, kUpRouted, used, red, n_units, tid);
+    few_grid_sync(a.arrivals + 1, &s.abort_flag, tid);
+    few_pass(f, kDownShared, used, red, n_units, tid);
+    few_pass(f, kDownRouted, used, red, n_units, tid);
+    few_grid_sync(a.arrivals + 2, &s.abort_flag, tid);
+    few_combine<X>(a, tid);
   } else if (copier) {
-    few_fill(f, cur, kUpRouted, 0xffffffffu, lane);
-    // the first stages of the down products, as the last of the up products are
-    // consumed: those copies run while the CTA waits for the others
-    few_fill(f, cur, kDownRouted, cur.issued + kFewStages, lane);
+    few_fill(f, cur, kDownRouted, lane);
+    if (lane == 0 && *static_cast<volatile int*>(&s.abort_flag)) {
+      // gave up a wait: let every copy land before the block ends
+      constexpr uint32_t kSlots = kFewStages / Few<WT>::kTeams;
+      int never = 0;
+      for (int t = 0; t < Few<WT>::kTeams; ++t) {
+        const uint32_t n = t ? cur.issued1 : cur.issued0;
+        for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i)
+          mbar_wait(&s.full[t * kSlots + i % kSlots], (i / kSlots) & 1u, &never);
+      }
+    }
   } else if (blockIdx.x == 0 && a.stats) {
     // the statistics, beside the other warps' work
     for (int e = lane; e < a.E; e += 32)
-      s.psum[e] = static_cast<unsigned long long>(__double_as_longlong(
-          balance_stats_expert(s.counts[e], s.psum[e], a.T, a.E, a.K, e, a.stats)));
+      s.fp[e] = balance_stats_expert(s.counts[e], __ldcg(a.psum + e), a.T, a.E, a.K, e, a.stats);
     __syncwarp();
     if (lane == 0) {
-      balance_loss(reinterpret_cast<const double*>(s.psum), a.E, a.alpha, a.stats);
+      balance_loss(s.fp, a.E, a.alpha, a.stats);
       if (a.extended) {
         double z = 0.0;
-        for (int i = 0; i < kFewWorkers / 32; ++i) z += s.zsum[i];
+        for (int t = 0; t < a.T; ++t) z += __ldcg(a.lse2 + t);
         utilisation_stats(s.counts, s.kept, a.E, a.T, z, a.stats);
       }
     }
   }
-  grid.sync();
-  if (worker) {
-    few_pass(f, kDownShared, used, red, n_units, tid);
-    few_pass(f, kDownRouted, used, red, n_units, tid);
-  } else if (copier) {
-    few_fill(f, cur, kDownRouted, 0xffffffffu, lane);
-  }
-  grid.sync();
-  if (worker) few_combine<X>(a, tid);
-  if (copier && lane == 0 && *static_cast<volatile int*>(&s.abort_flag)) {
-    // gave up a wait: let every copy land before the block ends
-    int never = 0;
-    for (uint32_t i = cur.issued > kFewStages ? cur.issued - kFewStages : 0; i < cur.issued; ++i)
-      mbar_wait(&s.full[i % kFewStages], (i / kFewStages) & 1u, &never);
-    raise_status(a.status, kDevWaitTimeout);
-  }
+  __syncthreads();
+  if (tid == 0 && *static_cast<volatile int*>(&s.abort_flag)) raise_status(a.status, kDevWaitTimeout);
 }
 
 // ----------------------------------------------------------------- host side
@@ -1013,6 +1092,8 @@ FewLayout make_few_layout(const Problem& p) {
   L.seg_off = take(static_cast<size_t>(p.E + 1) * 4);
   L.slot_of = take(TK * 4);
   L.perm = take(TK * 4);
+  L.psum = take(static_cast<size_t>(p.E) * 8);
+  L.lse2 = take(T * 4);
   L.amax = take((TK + T) * 4);
   L.h = take(TK * p.F * 4);
   L.h_s = take(T * p.Ns * p.F * 4);
@@ -1082,6 +1163,10 @@ cudaError_t launch_few_layer(const Problem& p, const FewCall& c, cudaStream_t st
   a.part = c.part;
   a.part_s = c.part_s;
   a.status = c.status;
+  a.arrivals = c.status + 16;
+  a.psum = c.psum;
+  a.lse2 = c.lse2;
+  a.spread = p.T > kFewWorkers / 32;
   a.T = static_cast<int>(p.T);
   a.d = p.d;
   a.E = p.E;

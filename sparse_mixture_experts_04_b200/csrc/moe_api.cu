@@ -320,6 +320,8 @@ static int few_impl(const Problem& p, FewCall c, const void* x, void* y, const m
   c.h = at<void>(ws, L.h);
   c.h_s = at<void>(ws, L.h_s);
   c.amax = at<unsigned>(ws, L.amax);
+  c.psum = at<unsigned long long>(ws, L.psum);
+  c.lse2 = at<float>(ws, L.lse2);
   c.part = at<float>(ws, L.part);
   c.part_s = at<float>(ws, L.part_s);
   c.status = at<unsigned>(ws, L.status);
