@@ -6,7 +6,8 @@
 // running from the first byte to the last instead of draining it at the ends
 // of six launches:
 //
-//   1. logits    tiles of 4 experts x 4 tokens over the CTAs        grid barrier
+//   1. logits    tiles of 4 experts x 4 tokens over the CTAs; with 8-bit
+//                weights also the tokens' integers                  grid barrier
 //   2. routing   softmax and top-K: up to 8 tokens every CTA for itself, more
 //                of them one token per CTA                          grid barrier
 //                capacity and slots: every CTA for itself; CTA 0 writes them
@@ -50,10 +51,12 @@ namespace moe {
 
 namespace cg = cooperative_groups;
 
+
 enum { kFewBF16 = 0, kFewF32 = 1, kFewI8 = 2 };
 
 constexpr int kFewWorkers = 256;                 // 8 warps
-constexpr int kFewThreads = kFewWorkers + 64;    // + a warp for the copies, a warp for the statistics
+constexpr int kFewCopiers = 2;                   // warps that issue copies, 16 / kFewCopiers rows of a stage each
+constexpr int kFewThreads = kFewWorkers + 32 * kFewCopiers + 32;  // + one warp for the statistics
 constexpr int kFewRows = 16;                     // weight rows of a unit
 constexpr int kFewChunk = 2048;                  // bytes of each row in a stage
 constexpr int kFewPitch = kFewChunk + 16;        // odd number of 16-byte pieces: no bank conflicts
@@ -109,6 +112,8 @@ struct FewArgs {
   float* stats;        // or nullptr
   void* h;             // [T K, F] hidden rows by slot: BF16, or FP32 (FP32 and 8-bit weights)
   void* h_s;           // [T, N_s F]
+  int8_t* x_q;         // 8-bit: the tokens' integers [T, d] and scales [T]
+  float* x_scale;
   unsigned* amax;      // 8-bit: bits of max|h| by slot, then by token for the shared experts
   float* part;         // [nc][T K][d] partial sums by slot
   float* part_s;       // [N_s nc][T][d]
@@ -300,7 +305,8 @@ struct Few {
   }
 };
 
-// The copy side (one warp, every lane alike).  Each team has its own ring of
+// The copy side (a warp for each half of a stage's rows, every lane alike).
+// Each team has its own ring of
 // kFewStages / teams stages, so that a team never waits for a phase of a barrier
 // more than one ahead (a parity wait could not tell it from the past one).  The
 // teams' units of a span are copied together, a stage of each in turn: stage k
@@ -316,7 +322,7 @@ struct Cursor {
 // Fill stages through pass last_pass (whose units are known by now); before the
 // routing (kUpShared) only the stages that are free, afterwards waiting for each.
 template <int WT>
-__device__ __forceinline__ void few_fill(const Few<WT>& f, Cursor& c, int last_pass, int lane) {
+__device__ __forceinline__ void few_fill(const Few<WT>& f, Cursor& c, int last_pass, int copier, int lane) {
   constexpr int kTeams = Few<WT>::kTeams, kSlots = kFewStages / kTeams;
   for (;;) {
     if (c.left == 0) {
@@ -343,11 +349,13 @@ __device__ __forceinline__ void few_fill(const Few<WT>& f, Cursor& c, int last_p
     const int col = c.q.col + c.team * c.q.step;
     const int rows = c.q.step == 8 ? kFewRows : min(kFewRows, c.q.cols - col);
     uint64_t* bar = &f.s.full[slot];
-    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(rows * bytes));
+    constexpr int kMine = kFewRows / kFewCopiers;
+    const int row = copier * kMine + lane;
+    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(max(0, min(kMine, rows - row)) * bytes));
     __syncwarp();
-    if (lane < rows) {
-      const char* src = c.q.w + (c.team * c.q.step + (lane & 7)) * c.q.row_bytes + (lane >> 3) * c.q.hi + c.off;
-      bulk_load(f.ring + slot * kFewStageBytes + lane * kFewPitch, src, static_cast<uint32_t>(bytes), bar);
+    if (lane < kMine && row < rows) {
+      const char* src = c.q.w + (c.team * c.q.step + (row & 7)) * c.q.row_bytes + (row >> 3) * c.q.hi + c.off;
+      bulk_load(f.ring + slot * kFewStageBytes + row * kFewPitch, src, static_cast<uint32_t>(bytes), bar);
     }
     if (c.team)
       ++c.issued1;
@@ -515,80 +523,139 @@ struct FewMath<kFewF32> {
 };
 
 // ---------------------------------------------------------------- token rows
-// Rows of the unit's group into the token buffer, zero behind the row's end up
-// to the next multiple of 64 bytes.  up: rows of x; down: a chunk of hidden rows.
+// What the token buffer holds: the same rows need no second load (one token:
+// every expert; the shared experts: every group).
+__device__ __forceinline__ int few_token_key(const FewArgs& a, const FewShared& s, int pass, const Span& q) {
+  if (pass > kUpRouted) return -1;
+  if (q.n == 1) return pass == kUpRouted ? s.perm[q.row0] / a.K : q.row0;
+  return pass == kUpShared ? (q.n << 16 | q.row0) : -1;
+}
+
+// Rows of the span's group into the token buffer, zero behind the row's end up
+// to the next multiple of 64 bytes.  up: rows of x (8-bit weights: its integers
+// from step 1); down: a chunk of hidden rows (8-bit weights: FP32, rounded to
+// integers here; every CTA has contributed to the row's largest magnitude).
+// Four 16-byte pieces per thread are in flight.
 template <int WT>
 __device__ __forceinline__ void few_load_tokens(const Few<WT>& f, int pass, const Span& q, int t_pitch, int tid) {
   const FewArgs& a = f.a;
   const bool up = pass <= kUpRouted;
   const bool routed = pass == kUpRouted || pass == kDownRouted;
-  const int pad = ((q.len + 63) & ~63) - q.len;
-  if constexpr (WT != kFewI8) {
-    const int vecs = q.len / 16, all = vecs + pad / 16;
-    for (int i = tid; i < q.n * all; i += kFewWorkers) {
-      const int r = i / all, v = i - r * all;
-      const char* src;
-      if (up) {
-        const int t = routed ? f.s.perm[q.row0 + r] / a.K : q.row0 + r;
-        src = static_cast<const char*>(a.x) + static_cast<int64_t>(t) * q.len;
-      } else if (routed) {
-        src = static_cast<const char*>(a.h) + (static_cast<int64_t>(q.row0 + r) * a.F) * Few<WT>::kW +
-              static_cast<int64_t>(q.c) * a.chunk_bytes;
-      } else {
-        src = static_cast<const char*>(a.h_s) +
-              (static_cast<int64_t>(q.row0 + r) * a.Ns + q.e) * a.F * Few<WT>::kW +
-              static_cast<int64_t>(q.c) * a.chunk_bytes;
-      }
-      const uint4 z = v < vecs ? __ldcg(reinterpret_cast<const uint4*>(src) + v) : make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(f.tok + r * t_pitch + v * 16) = z;
-    }
-  } else {
-    const int warp = tid >> 5, lane = tid & 31;
-    for (int r = warp; r < q.n; r += kFewWorkers / 32) {
-      uint8_t* dst = f.tok + r * t_pitch;
-      float scale;
-      if (up) {  // BF16 token row: its largest magnitude, then the integers
-        const int t = routed ? f.s.perm[q.row0 + r] / a.K : q.row0 + r;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) +
-                                                          static_cast<int64_t>(t) * a.d);
-        unsigned m = 0;
-        for (int v = lane; v < a.d / 8; v += 32) {
-          const uint4 w = src[v];
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  const int vecs = q.len / 16, all = ((q.len + 63) & ~63) / 16, total = q.n * all;
+  if (WT != kFewI8 || up) {
+    const char* base = static_cast<const char*>(up ? (WT == kFewI8 ? static_cast<const void*>(a.x_q) : a.x)
+                                                   : (routed ? a.h : a.h_s));
+    for (int i0 = tid; i0 < total; i0 += 4 * kFewWorkers) {
+      uint4 z[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) m = max(m, max((u[i] << 16) & 0x7FFF0000u, u[i] & 0x7FFF0000u));
-        }
-        scale = quant_scale(warp_max_u32(m));
-        const float inv = 1.0f / scale;
-        for (int v = lane; v < a.d / 8; v += 32) {
-          const uint4 w = src[v];
-          const float lo[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-          const float hi[4] = {bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
-          *reinterpret_cast<uint2*>(dst + v * 8) =
-              make_uint2(quant_pack4(lo, scale, inv), quant_pack4(hi, scale, inv));
-        }
-      } else {  // FP32 hidden row whose largest magnitude every CTA has contributed to
-        const int64_t row = q.row0 + r;
-        const float* src = (routed ? static_cast<const float*>(a.h) + row * a.F
-                                   : static_cast<const float*>(a.h_s) + (row * a.Ns + q.e) * a.F) +
-                           static_cast<int64_t>(q.c) * a.chunk_bytes;
-        scale = quant_scale(__ldcg(a.amax + (routed ? row : static_cast<int64_t>(a.T) * a.K + row)));
-        const float inv = 1.0f / scale;
-        for (int v = lane; v < q.len / 4; v += 32) {
-          const float4 w = __ldcg(reinterpret_cast<const float4*>(src) + v);
-          const float z[4] = {w.x, w.y, w.z, w.w};
-          *reinterpret_cast<uint32_t*>(dst + v * 4) = quant_pack4(z, scale, inv);
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * kFewWorkers, r = i / all, v = i - r * all;
+        z[j] = make_uint4(0, 0, 0, 0);
+        if (i < total && v < vecs) {
+          int64_t at;
+          if (up)
+            at = static_cast<int64_t>(routed ? f.s.perm[q.row0 + r] / a.K : q.row0 + r) * q.len;
+          else
+            at = (routed ? q.row0 + r : static_cast<int64_t>(q.row0 + r) * a.Ns + q.e) * a.F * Few<WT>::kW +
+                 static_cast<int64_t>(q.c) * a.chunk_bytes;
+          z[j] = __ldcg(reinterpret_cast<const uint4*>(base + at) + v);
         }
       }
-      if (lane < pad / 16) *reinterpret_cast<uint4*>(dst + q.len + lane * 16) = make_uint4(0, 0, 0, 0);
-      if (lane == 0) f.s.row_scale[r] = scale;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * kFewWorkers, r = i / all, v = i - r * all;
+        if (i < total) *reinterpret_cast<uint4*>(f.tok + r * t_pitch + v * 16) = z[j];
+      }
+    }
+    if (WT == kFewI8 && tid < q.n)
+      f.s.row_scale[tid] = __ldcg(a.x_scale + (routed ? f.s.perm[q.row0 + tid] / a.K : q.row0 + tid));
+  } else {
+    for (int i = tid; i < total; i += kFewWorkers) {
+      const int r = i / all, v = i - r * all;
+      const int64_t row = q.row0 + r;
+      const float4* src = reinterpret_cast<const float4*>(
+          (routed ? static_cast<const float*>(a.h) + row * a.F
+                  : static_cast<const float*>(a.h_s) + (row * a.Ns + q.e) * a.F) +
+          static_cast<int64_t>(q.c) * a.chunk_bytes) + v * 4;
+      uint32_t w[4] = {0, 0, 0, 0};
+      float4 z[4];
+      const unsigned m = __ldcg(a.amax + (routed ? row : static_cast<int64_t>(a.T) * a.K + row));
+      if (v < vecs) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = __ldcg(src + j);
+      }
+      const float scale = quant_scale(m), inv = 1.0f / scale;
+      if (v < vecs) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e[4] = {z[j].x, z[j].y, z[j].z, z[j].w};
+          w[j] = quant_pack4(e, scale, inv);
+        }
+      }
+      *reinterpret_cast<uint4*>(f.tok + r * t_pitch + v * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (v == 0) f.s.row_scale[r] = scale;
     }
   }
 }
 
+// 8-bit weights: the integers and the scale of token t (one CTA's workers).
+__device__ __forceinline__ void few_quantize_token(const FewArgs& a, int t, unsigned* s_max, int tid) {
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) +
+                                                    static_cast<int64_t>(t) * a.d);
+  const int vecs = a.d / 8;
+  unsigned m = 0;
+#pragma unroll 4
+  for (int v = tid; v < vecs; v += kFewWorkers) {
+    const uint4 w = src[v];
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max((u[i] << 16) & 0x7FFF0000u, u[i] & 0x7FFF0000u));
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((tid & 31) == 0) s_max[tid >> 5] = m;
+  named_bar_sync(1, kFewWorkers);
+#pragma unroll
+  for (int i = 0; i < kFewWorkers / 32; ++i) m = max(m, s_max[i]);
+  const float scale = quant_scale(m), inv = 1.0f / scale;
+  uint2* dst = reinterpret_cast<uint2*>(a.x_q + static_cast<int64_t>(t) * a.d);
+#pragma unroll 4
+  for (int v = tid; v < vecs; v += kFewWorkers) {
+    const uint4 w = src[v];
+    const float lo[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+    const float hi[4] = {bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
+    dst[v] = make_uint2(quant_pack4(lo, scale, inv), quant_pack4(hi, scale, inv));
+  }
+  if (tid == 0) a.x_scale[t] = scale;
+  named_bar_sync(1, kFewWorkers);
+}
+
 // ------------------------------------------------------------- unit outputs
+// 8-bit weights: the scales of the unit's rows that thread tid of the team
+// stores, at row offset `ahead` (up: a gate and an up row; down: one channel).
 template <int WT>
-__device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const Span& q, const void* red, int tid) {
+__device__ __forceinline__ float2 few_scales(const Few<WT>& f, int pass, const Span& q, int ahead, int tid) {
+  const FewArgs& a = f.a;
+  float2 v = make_float2(0.f, 0.f);
+  if constexpr (WT == kFewI8) {
+    if (pass <= kUpRouted) {
+      const int col = q.col + ahead + (tid & 7);
+      if (col < q.cols) {
+        const float* sc = (pass == kUpShared ? a.s13_s : a.s13) + static_cast<int64_t>(q.e) * 2 * a.F + col;
+        v.x = __ldg(sc);
+        v.y = __ldg(sc + a.F);
+      }
+    } else {
+      const int col = q.col + ahead + (tid & 15);
+      if (col < q.cols) v.x = __ldg(pass == kDownShared ? a.s2_s + col : a.s2 + static_cast<int64_t>(q.e) * a.d + col);
+    }
+  }
+  return v;
+}
+
+// sc: few_scales of this unit
+template <int WT>
+__device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const Span& q, const void* red, float2 sc,
+                                               int tid) {
   using M = FewMath<WT>;
   const FewArgs& a = f.a;
   if (pass <= kUpRouted) {  // 8 features x n tokens: lane groups of 8 share a token
@@ -597,10 +664,9 @@ __device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const
     float h = 0.f;
     if (live) {
       if constexpr (WT == kFewI8) {
-        const float* sc = (pass == kUpShared ? a.s13_s : a.s13) + static_cast<int64_t>(q.e) * 2 * a.F + q.col + ft;
         const float sx = f.s.row_scale[tok];
-        const float g = __int2float_rn(M::get(red, ft, tok)) * (sx * sc[0]);
-        const float u = __int2float_rn(M::get(red, ft + 8, tok)) * (sx * sc[a.F]);
+        const float g = __int2float_rn(M::get(red, ft, tok)) * (sx * sc.x);
+        const float u = __int2float_rn(M::get(red, ft + 8, tok)) * (sx * sc.y);
         h = silu(g) * u;
       } else {
         h = silu(M::get(red, ft, tok)) * M::get(red, ft + 8, tok);
@@ -623,13 +689,10 @@ __device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const
   } else {  // 16 output channels x n tokens
     const int n = tid & 15;
     if (q.col + n >= q.cols) return;
-    float sw = 0.f;
-    if constexpr (WT == kFewI8)
-      sw = pass == kDownShared ? a.s2_s[q.col + n] : a.s2[static_cast<int64_t>(q.e) * a.d + q.col + n];
     for (int tok = tid >> 4; tok < q.n; tok += Few<WT>::kTeamWarps * 2) {
       float v;
       if constexpr (WT == kFewI8)
-        v = __int2float_rn(M::get(red, n, tok)) * (f.s.row_scale[tok] * sw);
+        v = __int2float_rn(M::get(red, n, tok)) * (f.s.row_scale[tok] * sc.x);
       else
         v = M::get(red, n, tok);
       const int64_t row = q.row0 + tok;
@@ -645,7 +708,7 @@ __device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const
 // takes units t, t + teams, ... of a span; `used`: stages this team has consumed.
 template <int WT>
 __device__ __forceinline__ void few_pass(const Few<WT>& f, int pass, uint32_t& used, uint8_t* red_base,
-                                         uint32_t& n_units, int tid) {
+                                         uint32_t& n_units, int& held, int tid) {
   constexpr int kTeams = Few<WT>::kTeams, kWarps = Few<WT>::kTeamWarps, kSlots = kFewStages / kTeams;
   const int lane = tid & 31, team = (tid >> 5) / kWarps, warp = (tid >> 5) % kWarps;
   const PassRange r = f.range(pass);
@@ -655,13 +718,24 @@ __device__ __forceinline__ void few_pass(const Few<WT>& f, int pass, uint32_t& u
     Span q = f.span(pass, u, r.last);
     u += q.units;
     const int t_pitch = ((q.len + 63) & ~63) + 16;
-    // the last unit's reads of the token buffer (and of the row scales) are
-    // over only once its outputs are stored
-    named_bar_sync(1, kFewWorkers);
-    few_load_tokens(f, pass, q, t_pitch, tid);
-    named_bar_sync(1, kFewWorkers);
+    const int key = few_token_key(f.a, f.s, pass, q);
+    if (key < 0 || key != held) {
+      // the last unit's reads of the token buffer (and of the row scales) are
+      // over only once its outputs are stored
+      named_bar_sync(1, kFewWorkers);
+      few_load_tokens(f, pass, q, t_pitch, tid);
+      named_bar_sync(1, kFewWorkers);
+      held = key;
+    }
     q.col += team * q.step;
+    // 8-bit weights: the scales are fetched one unit ahead (fetched when needed
+    // they cost the team a memory latency per unit: 210 -> 200 us for 7 tokens
+    // of d = 4096, E = 128, F = 1536)
+    const int team_tid = tid - team * kWarps * 32;
+    float2 sc_next = few_scales(f, pass, q, 0, team_tid);
     for (int i = team; i < q.units; i += kTeams) {
+      const float2 sc = sc_next;
+      if (i + kTeams < q.units) sc_next = few_scales(f, pass, q, kTeams * q.step, team_tid);
       math.clear();
       uint8_t* red = red_base + (n_units & 1u) * (kFewRedBytes / kTeams / 2);
       const int rows = min(kFewRows, q.step == 8 ? kFewRows : q.cols - q.col);
@@ -676,7 +750,7 @@ __device__ __forceinline__ void few_pass(const Few<WT>& f, int pass, uint32_t& u
       }
       math.put(red, q.n, warp, lane);
       named_bar_sync(2 + team, kWarps * 32);  // the unit's sums are complete
-      few_store_unit(f, pass, q, red, tid - team * kWarps * 32);
+      few_store_unit(f, pass, q, red, sc, team_tid);
       q.col += kTeams * q.step;
       ++n_units;  // the next unit's sums go to the other half: no barrier before they are written
     }
@@ -864,62 +938,54 @@ __device__ __forceinline__ void few_dispatch(const FewArgs& a, FewShared& s, con
 }
 
 // y_t = sum over the shared experts' chunks + sum_k w_k (sum of Expert_k's
-// chunks), k ascending; the loads of four addends at a time are in flight.
+// chunks), k ascending; the loads of eight addends at a time are in flight.
+// slot, w: the tokens' slots and gates in shared memory.
 template <typename T>
-__device__ __forceinline__ void few_combine(const FewArgs& a, int tid) {
+__device__ __forceinline__ void few_combine(const FewArgs& a, const int32_t* slot, const float* w, int tid) {
+  constexpr int kFly = 8;
   const int vecs = a.d / 4;
   const int total = a.T * vecs;
 #pragma unroll 1
   for (int i = blockIdx.x * kFewWorkers + tid; i < total; i += gridDim.x * kFewWorkers) {
     const int t = i / vecs, c = (i - t * vecs) * 4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int ns = a.Ns * a.nc, nr = a.K * a.nc;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), e = acc;
+    // addends: the shared experts' chunks, then each choice's
+    const int ns = a.Ns * a.nc, nr = ns + a.K * a.nc;
+    int n = 0, k = 0;
 #pragma unroll 1
-    for (int n0 = 0; n0 < ns; n0 += 4) {
-      float4 v[4];
+    for (int m0 = 0; m0 < nr; m0 += kFly) {
+      float4 v[kFly];
+      int of[kFly];  // choice the addend ends, or -1
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kFly; ++j) {
+        const int m = m0 + j;
         v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (n0 + j < ns)
-          v[j] = __ldcg(reinterpret_cast<const float4*>(a.part_s + (static_cast<int64_t>(n0 + j) * a.T + t) * a.d + c));
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc.x += v[j].x; acc.y += v[j].y; acc.z += v[j].z; acc.w += v[j].w;
-      }
-    }
-    float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
-    int n = 0, k = 0;  // next addend: chunk n of the k-th choice
-#pragma unroll 1
-    for (int m0 = 0; m0 < nr; m0 += 4) {
-      float4 v[4];
-      float w[4];
-      bool last[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        w[j] = 0.f;
-        last[j] = false;
-        if (m0 + j < nr) {
-          const int slot = __ldcg(a.slot_of + t * a.K + k);
-          if (slot >= 0) {
-            v[j] = __ldcg(reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(n) * a.T * a.K + slot) * a.d + c));
-            w[j] = __ldcg(a.topk_w + t * a.K + k);
-          }
-          last[j] = slot >= 0 && n + 1 == a.nc;
+        of[j] = -1;
+        if (m < ns) {
+          v[j] = __ldcg(reinterpret_cast<const float4*>(a.part_s + (static_cast<int64_t>(m) * a.T + t) * a.d + c));
+        } else if (m < nr) {
+          const int sl = slot[t * a.K + k];
+          if (sl >= 0)
+            v[j] = __ldcg(reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(n) * a.T * a.K + sl) * a.d + c));
           if (++n == a.nc) {
+            of[j] = sl >= 0 ? k : -1;
             n = 0;
             ++k;
           }
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        e.x += v[j].x; e.y += v[j].y; e.z += v[j].z; e.w += v[j].w;
-        if (last[j]) {
-          acc.x = fmaf(w[j], e.x, acc.x); acc.y = fmaf(w[j], e.y, acc.y);
-          acc.z = fmaf(w[j], e.z, acc.z); acc.w = fmaf(w[j], e.w, acc.w);
-          e = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int j = 0; j < kFly; ++j) {
+        if (m0 + j < ns) {
+          acc.x += v[j].x; acc.y += v[j].y; acc.z += v[j].z; acc.w += v[j].w;
+        } else {
+          e.x += v[j].x; e.y += v[j].y; e.z += v[j].z; e.w += v[j].w;
+          if (of[j] >= 0) {
+            const float g = w[t * a.K + of[j]];
+            acc.x = fmaf(g, e.x, acc.x); acc.y = fmaf(g, e.y, acc.y);
+            acc.z = fmaf(g, e.z, acc.z); acc.w = fmaf(g, e.w, acc.w);
+            e = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
         }
       }
     }
@@ -942,11 +1008,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   FewShared& s = *reinterpret_cast<FewShared*>(red + kFewRedBytes);
   cg::grid_group grid = cg::this_grid();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool worker = warp < kFewWorkers / 32, copier = warp == kFewWorkers / 32;
+  const int copier = warp - kFewWorkers / 32;  // 0 .. kFewCopiers - 1: a copying warp
+  const bool worker = copier < 0, copies = copier >= 0 && copier < kFewCopiers;
 
   if (tid == 0) {
     for (int i = 0; i < kFewStages; ++i) {
-      mbar_init(&s.full[i], 1);
+      mbar_init(&s.full[i], kFewCopiers);
       mbar_init(&s.empty[i], Few<WT>::kTeamWarps);
     }
     s.abort_flag = 0;
@@ -966,13 +1033,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   const Few<WT> f(a, s, ring, tok);
   Cursor cur;
   uint32_t used = 0, n_units = 0;
-  if (copier) {  // the shared experts' weights do not wait for the routing
+  int held = -1;
+  if (copies) {  // the shared experts' weights do not wait for the routing
     const PassRange r = f.range(kUpShared);
     cur.u = r.first;
     cur.end = r.last;
-    few_fill(f, cur, kUpShared, lane);
+    few_fill(f, cur, kUpShared, copier, lane);
   }
-  if (worker && !a.given) few_logits<X>(a, reinterpret_cast<double*>(red), tid);
+  if (worker) {
+    if (!a.given) few_logits<X>(a, reinterpret_cast<double*>(red), tid);
+    if constexpr (WT == kFewI8) {  // the last CTAs first: the first ones have the logits' tiles
+      for (int t = gridDim.x - 1 - blockIdx.x; t < a.T; t += gridDim.x)
+        few_quantize_token(a, t, reinterpret_cast<unsigned*>(red), tid);
+    }
+  }
   grid.sync();
 
   if (worker) {
@@ -995,15 +1069,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   }
   __syncthreads();
   if (worker) {
-    few_pass(f, kUpShared, used, red, n_units, tid);
-    few_pass(f, kUpRouted, used, red, n_units, tid);
+    few_pass(f, kUpShared, used, red, n_units, held, tid);
+    few_pass(f, kUpRouted, used, red, n_units, held, tid);
     few_grid_sync(a.arrivals + 1, &s.abort_flag, tid);
-    few_pass(f, kDownShared, used, red, n_units, tid);
-    few_pass(f, kDownRouted, used, red, n_units, tid);
+    few_pass(f, kDownShared, used, red, n_units, held, tid);
+    few_pass(f, kDownRouted, used, red, n_units, held, tid);
+    // the gates, while the other CTAs finish
+    named_bar_sync(1, kFewWorkers);
+    int32_t* slot = reinterpret_cast<int32_t*>(tok);
+    float* gate = reinterpret_cast<float*>(tok) + kFewMaxPairs;
+#pragma unroll 1
+    for (int i = tid; i < a.T * a.K; i += kFewWorkers) {
+      slot[i] = __ldcg(a.slot_of + i);
+      gate[i] = __ldcg(a.topk_w + i);
+    }
     few_grid_sync(a.arrivals + 2, &s.abort_flag, tid);
-    few_combine<X>(a, tid);
-  } else if (copier) {
-    few_fill(f, cur, kDownRouted, lane);
+    few_combine<X>(a, slot, gate, tid);
+  } else if (copies) {
+    few_fill(f, cur, kDownRouted, copier, lane);
     if (lane == 0 && *static_cast<volatile int*>(&s.abort_flag)) {
       // gave up a wait: let every copy land before the block ends
       constexpr uint32_t kSlots = kFewStages / Few<WT>::kTeams;
@@ -1061,9 +1144,13 @@ static void few_tiling(const Problem& p, bool i8, FewArgs* a) {
   const int64_t fb = p.F * ws;
   const int64_t want = p.T < 8 ? p.T : 8;
   int64_t longest = (kFewTokBytes / want - 80) / kFewChunk * kFewChunk;
+  // nor longer than 8 KB, so that every CTA gets many units: with one chunk of
+  // 28 KB (F = 14336, one token) a CTA had 3 or 4 units and the down product
+  // ended 15% late
+  if (longest > 4 * kFewChunk) longest = 4 * kFewChunk;
   a->nc = static_cast<int>((fb + longest - 1) / longest);
   const int64_t even = (fb + a->nc - 1) / a->nc;
-  const int64_t chunk = (even + kFewChunk - 1) / kFewChunk * kFewChunk;
+  const int64_t chunk = (even + 63) / 64 * 64;  // chunks of equal length: units of equal cost
   a->nc = static_cast<int>((fb + chunk - 1) / chunk);
   a->chunk_bytes = static_cast<int>(chunk);
   a->ng_down = rows(fb < chunk ? fb : chunk);
@@ -1094,6 +1181,8 @@ FewLayout make_few_layout(const Problem& p) {
   L.perm = take(TK * 4);
   L.psum = take(static_cast<size_t>(p.E) * 8);
   L.lse2 = take(T * 4);
+  L.x_q = take(T * p.d);
+  L.x_scale = take(T * 4);
   L.amax = take((TK + T) * 4);
   L.h = take(TK * p.F * 4);
   L.h_s = take(T * p.Ns * p.F * 4);
@@ -1159,6 +1248,8 @@ cudaError_t launch_few_layer(const Problem& p, const FewCall& c, cudaStream_t st
   a.stats = c.stats;
   a.h = c.h;
   a.h_s = c.h_s;
+  a.x_q = c.x_q;
+  a.x_scale = c.x_scale;
   a.amax = c.amax;
   a.part = c.part;
   a.part_s = c.part_s;

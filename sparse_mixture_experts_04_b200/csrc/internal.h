@@ -153,7 +153,7 @@ int launch_up_projections(const Problem& p, int mode, const void* x_rows, int64_
 // Byte offsets of its scratch in the caller's workspace (either weight type).
 struct FewLayout {
   size_t status, logits, topk_idx, topk_w, counts, kept, seg_off, slot_of, perm;
-  size_t psum, lse2, amax, h, h_s, part, part_s;  // status: 256 bytes, the grid barriers' counts in them
+  size_t psum, lse2, x_q, x_scale, amax, h, h_s, part, part_s;  // status: 256 bytes, the grid barriers' counts in them
   size_t total;
 };
 bool few_supported(const Problem& p, bool i8);
@@ -171,6 +171,8 @@ struct FewCall {
   int32_t *counts, *kept, *seg_off, *slot_of, *perm;
   float* stats;  // or nullptr
   void *h, *h_s;
+  int8_t* x_q;
+  float* x_scale;
   unsigned* amax;
   unsigned long long* psum;
   float *lse2, *part, *part_s;

@@ -319,6 +319,8 @@ static int few_impl(const Problem& p, FewCall c, const void* x, void* y, const m
   c.stats = stats;
   c.h = at<void>(ws, L.h);
   c.h_s = at<void>(ws, L.h_s);
+  c.x_q = at<int8_t>(ws, L.x_q);
+  c.x_scale = at<float>(ws, L.x_scale);
   c.amax = at<unsigned>(ws, L.amax);
   c.psum = at<unsigned long long>(ws, L.psum);
   c.lse2 = at<float>(ws, L.lse2);
