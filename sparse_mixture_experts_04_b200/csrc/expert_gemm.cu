@@ -54,11 +54,17 @@ namespace moe {
 //   EPI_I8_OUT    : y = (sum) * a_scale[row] * b_scale[column], BF16 or FP32
 enum { EPI_SWIGLU = 0, EPI_BF16 = 1, EPI_F32 = 2, EPI_I8_SWIGLU = 3, EPI_I8_OUT = 4 };
 __host__ __device__ constexpr bool is_i8(int epi) { return epi == EPI_I8_SWIGLU || epi == EPI_I8_OUT; }
+// Epilogue warps.  The 8-bit products have eight, two for each quarter of the
+// TMEM lanes, each with half of the tile's columns: their main loop takes half
+// the time of BF16's for the same tile, and with one warp per scheduler the
+// epilogue's latencies (TMEM, scales) set the pace (65536 rows, K = 2048,
+// N = 2816, 64 groups: 605 us with four, tensor pipe 30% busy).
+__host__ __device__ constexpr int epilogue_warps(int epi) { return is_i8(epi) ? 8 : 4; }
+__host__ __device__ constexpr int gemm_threads(int epi) { return 64 + 32 * epilogue_warps(epi); }
 __host__ __device__ constexpr bool is_swiglu(int epi) { return epi == EPI_SWIGLU || epi == EPI_I8_SWIGLU; }
 
 constexpr int kBM = 128;
 constexpr int kBK = 64;  // 64 BF16 = 128 bytes: one 128-byte swizzle row
-constexpr int kGemmThreads = 192;
 constexpr int kMaxGroups = 256;
 
 struct GemmArgs {
@@ -308,61 +314,6 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs& args, int g, int r
         }
       }
     }
-  } else if constexpr (EPI == EPI_I8_SWIGLU) {
-    float* out_row = static_cast<float*>(args.out) + static_cast<int64_t>(row) * args.ldo +
-                     static_cast<int64_t>(g) * args.out_col_stride;
-    const float* bs = args.b_scale + g * args.b_scale_stride;
-    const float sa = row_ok ? args.a_scale[row] : 0.f;
-    unsigned amax = 0;
-#pragma unroll 1
-    for (int c = 0; c < BN / 2; c += 32) {
-      uint32_t gr[32], ur[32];
-      tmem_load_32x32(t_row + c, gr);
-      tmem_load_32x32(t_row + BN / 2 + c, ur);
-      tmem_load_wait();
-      if (row_ok) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int col = n0 + c + q * 4;
-          if (col < args.N) {
-            const float4 sg = *reinterpret_cast<const float4*>(bs + col);
-            const float4 su = *reinterpret_cast<const float4*>(bs + args.N + col);
-            const float h0 = i8_silu_mul(gr[q * 4], ur[q * 4], sa, sg.x, su.x);
-            const float h1 = i8_silu_mul(gr[q * 4 + 1], ur[q * 4 + 1], sa, sg.y, su.y);
-            const float h2 = i8_silu_mul(gr[q * 4 + 2], ur[q * 4 + 2], sa, sg.z, su.z);
-            const float h3 = i8_silu_mul(gr[q * 4 + 3], ur[q * 4 + 3], sa, sg.w, su.w);
-            amax = max(max(amax, max(abs_bits(h0), abs_bits(h1))), max(abs_bits(h2), abs_bits(h3)));
-            *reinterpret_cast<float4*>(out_row + col) = make_float4(h0, h1, h2, h3);
-          }
-        }
-      }
-    }
-    if (row_ok) atomicMax(args.row_amax + row, amax);
-  } else if constexpr (EPI == EPI_I8_OUT) {
-    const int64_t at = static_cast<int64_t>(row) * args.ldo + static_cast<int64_t>(g) * args.out_col_stride;
-    const float* bs = args.b_scale + g * args.b_scale_stride;
-    const float sa = row_ok ? args.a_scale[row] : 0.f;
-#pragma unroll 1
-    for (int c = 0; c < BN; c += 32) {
-      uint32_t vr[32];
-      tmem_load_32x32(t_row + c, vr);
-      tmem_load_wait();
-      if (row_ok) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int col = n0 + c + q * 8;
-          if (col < args.N) {
-            const float4 s0 = *reinterpret_cast<const float4*>(bs + col);
-            const float4 s1 = *reinterpret_cast<const float4*>(bs + col + 4);
-            const float sb[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __int2float_rn(static_cast<int>(vr[q * 8 + j])) * (sa * sb[j]);
-            i8_store8(args, at + col, v);
-          }
-        }
-      }
-    }
   } else if (EPI == EPI_BF16) {
     __nv_bfloat16* out_row = static_cast<__nv_bfloat16*>(args.out) + static_cast<int64_t>(row) * args.ldo +
                              static_cast<int64_t>(g) * args.out_col_stride;
@@ -405,6 +356,99 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs& args, int g, int r
   }
 }
 
+// The 8-bit epilogues of one warp: its 32 TMEM lanes, half `half` of the tile's
+// BN columns, whose first is at t_row.  The next block's TMEM load is in flight
+// while one block is scaled and stored.
+template <int BN>
+__device__ __forceinline__ void epilogue_i8_out(const GemmArgs& args, int g, int row, bool row_ok, int n0,
+                                                uint32_t t_row, int half) {
+  const int64_t at = static_cast<int64_t>(row) * args.ldo + static_cast<int64_t>(g) * args.out_col_stride;
+  const float* bs = args.b_scale + g * args.b_scale_stride;
+  const float sa = row_ok ? args.a_scale[row] : 0.f;
+  const int c0 = half * (BN / 2), c1 = min(c0 + BN / 2, args.N - n0);
+  auto block = [&](const uint32_t (&v)[32], int c) {
+    if (!row_ok) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int col = n0 + c + q * 8;
+      if (col < args.N) {
+        const float4 s0 = __ldg(reinterpret_cast<const float4*>(bs + col));
+        const float4 s1 = __ldg(reinterpret_cast<const float4*>(bs + col) + 1);
+        const float sb[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = __int2float_rn(static_cast<int>(v[q * 8 + j])) * (sa * sb[j]);
+        i8_store8(args, at + col, y);
+      }
+    }
+  };
+  if (c0 >= c1) return;
+  uint32_t va[32], vb[32];
+  tmem_load_32x32(t_row + c0, va);
+  tmem_load_wait();
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 64) {
+    if (c + 32 < c1) tmem_load_32x32(t_row + c + 32, vb);
+    block(va, c);
+    tmem_load_wait();
+    if (c + 32 >= c1) break;
+    if (c + 64 < c1) tmem_load_32x32(t_row + c + 64, va);
+    block(vb, c + 32);
+    tmem_load_wait();
+  }
+}
+
+template <int BN>
+__device__ __forceinline__ void epilogue_i8_swiglu(const GemmArgs& args, int g, int row, bool row_ok, int n0,
+                                                   uint32_t t_row, int half) {
+  float* out_row = static_cast<float*>(args.out) + static_cast<int64_t>(row) * args.ldo +
+                   static_cast<int64_t>(g) * args.out_col_stride;
+  const float* bs = args.b_scale + g * args.b_scale_stride;
+  const float sa = row_ok ? args.a_scale[row] : 0.f;
+  unsigned amax = 0;
+  const int c0 = half * (BN / 4), c1 = min(c0 + BN / 4, args.N - n0);
+  auto block = [&](const uint32_t (&gr)[16], const uint32_t (&ur)[16], int c) {
+    if (!row_ok) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int col = n0 + c + q * 4;
+      if (col < args.N) {
+        const float4 sg = __ldg(reinterpret_cast<const float4*>(bs + col));
+        const float4 su = __ldg(reinterpret_cast<const float4*>(bs + args.N + col));
+        const float h0 = i8_silu_mul(gr[q * 4], ur[q * 4], sa, sg.x, su.x);
+        const float h1 = i8_silu_mul(gr[q * 4 + 1], ur[q * 4 + 1], sa, sg.y, su.y);
+        const float h2 = i8_silu_mul(gr[q * 4 + 2], ur[q * 4 + 2], sa, sg.z, su.z);
+        const float h3 = i8_silu_mul(gr[q * 4 + 3], ur[q * 4 + 3], sa, sg.w, su.w);
+        amax = max(max(amax, max(abs_bits(h0), abs_bits(h1))), max(abs_bits(h2), abs_bits(h3)));
+        *reinterpret_cast<float4*>(out_row + col) = make_float4(h0, h1, h2, h3);
+      }
+    }
+  };
+  if (c0 < c1) {
+    uint32_t ga[16], ua[16], gb[16], ub[16];
+    tmem_load_32x16(t_row + c0, ga);
+    tmem_load_32x16(t_row + BN / 2 + c0, ua);
+    tmem_load_wait();
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 32) {
+      if (c + 16 < c1) {
+        tmem_load_32x16(t_row + c + 16, gb);
+        tmem_load_32x16(t_row + BN / 2 + c + 16, ub);
+      }
+      block(ga, ua, c);
+      tmem_load_wait();
+      if (c + 16 >= c1) break;
+      if (c + 32 < c1) {
+        tmem_load_32x16(t_row + c + 32, ga);
+        tmem_load_32x16(t_row + BN / 2 + c + 32, ua);
+      }
+      block(gb, ub, c + 16);
+      tmem_load_wait();
+    }
+  }
+  if (row_ok && amax) atomicMax(args.row_amax + row, amax);
+}
+
 // FP32 epilogue through shared memory: each 32-column block of this warp's 32
 // accumulator rows goes lane-per-row into xw (XOR-swizzled, no bank
 // conflicts) and out lane-per-column, so every store instruction writes 32
@@ -435,7 +479,7 @@ __device__ __forceinline__ void epilogue_f32_staged(const GemmArgs& args, int g,
 }
 
 template <int EPI, int BN, int STAGES>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(gemm_threads(EPI), 1)
     grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                            const __grid_constant__ GemmArgs args, const __grid_constant__ CUtensorMap tmA_2,
                            const __grid_constant__ CUtensorMap tmB_2, const __grid_constant__ GemmArgs args2) {
@@ -467,7 +511,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 4);
+      mbar_init(&tempty[a], epilogue_warps(EPI));
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -621,6 +665,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (EPI == EPI_F32)
         epilogue_f32_staged<BN>(ti.second ? args2 : args, ti.g, ti.row0 + quarter * 32, ti.row_end, t_row, lane,
                                 xw_all + quarter * 32 * 32);
+      else if constexpr (EPI == EPI_I8_SWIGLU)
+        epilogue_i8_swiglu<BN>(ti.second ? args2 : args, ti.g, row, row < ti.row_end, ti.n0, t_row, (warp - 2) >> 2);
+      else if constexpr (EPI == EPI_I8_OUT)
+        epilogue_i8_out<BN>(ti.second ? args2 : args, ti.g, row, row < ti.row_end, ti.n0, t_row, (warp - 2) >> 2);
       else
         epilogue_rows<EPI, BN>(ti.second ? args2 : args, ti.g, row, row < ti.row_end, ti.n0, t_row);
       tc_fence_before_sync();
@@ -838,7 +886,7 @@ __device__ __forceinline__ void epilogue_swap(const GemmArgs& args, const TileIn
 }
 
 template <int EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1)
     grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                              const __grid_constant__ CUtensorMap tmA64, const __grid_constant__ CUtensorMap tmB64,
                              const __grid_constant__ CUtensorMap tmA32, const __grid_constant__ CUtensorMap tmA16,
@@ -880,7 +928,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 8);
+      mbar_init(&tempty[a], 2 * epilogue_warps(EPI));
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -1105,16 +1153,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const uint32_t acc_par = static_cast<uint32_t>(it >> 1) & 1u;
       // all four epilogue warps take the same decision (a swap tile's
       // epilogue synchronises them), even when a wait gives up
-      const bool ready = named_bar_and(2, 128, mbar_wait(&tfull[acc], acc_par, abort_flag));
+      const bool ready =
+          named_bar_and(2, 32 * epilogue_warps(EPI), mbar_wait(&tfull[acc], acc_par, abort_flag));
       if (!ready) break;
       tc_fence_after_sync();
       const uint32_t t_row =
           tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * kPairBN);
+      const int half = (warp - 2) >> 2;  // 8-bit products: the second four warps
       if (ti.swap) {
-        epilogue_swap<EPI>(A, ti, rank, quarter, lane, (warp - 2) * 32 + lane, t_row, xbuf);
+        if (half == 0) epilogue_swap<EPI>(A, ti, rank, quarter, lane, (warp - 2) * 32 + lane, t_row, xbuf);
       } else {
         const int row = ti.row0 + 128 * static_cast<int>(rank) + r;
-        epilogue_rows<EPI, kPairBN>(A, ti.g, row, row < ti.row_end, ti.n0, t_row);
+        if constexpr (EPI == EPI_I8_SWIGLU)
+          epilogue_i8_swiglu<kPairBN>(A, ti.g, row, row < ti.row_end, ti.n0, t_row, half);
+        else if constexpr (EPI == EPI_I8_OUT)
+          epilogue_i8_out<kPairBN>(A, ti.g, row, row < ti.row_end, ti.n0, t_row, half);
+        else
+          epilogue_rows<EPI, kPairBN>(A, ti.g, row, row < ti.row_end, ti.n0, t_row);
       }
       tc_fence_before_sync();
       __syncwarp();
@@ -1287,7 +1342,7 @@ static int run_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const GemmArgs
   // without a second problem its maps are the first's (never read: no tiles)
   GemmArgs b = two ? *a2 : a;
   if (!two) b.n_groups = 0;
-  return launch_k(grouped_gemm_tc_kernel<EPI, BN, STAGES>, dim3(static_cast<unsigned>(grid)), dim3(kGemmThreads),
+  return launch_k(grouped_gemm_tc_kernel<EPI, BN, STAGES>, dim3(static_cast<unsigned>(grid)), dim3(gemm_threads(EPI)),
                   smem, st, ta, tb, a, two ? *ta2 : ta, two ? *tb2 : tb, b) == cudaSuccess ? 0 : -3;
 }
 
@@ -1319,7 +1374,7 @@ static int run_pair_gemm(const PairProblem& p1, const PairProblem* p2, cudaStrea
       // a persistent grid must fit at once: ask how many 2-CTA clusters can be co-resident
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
-      cfg.blockDim = dim3(kGemmThreads, 1, 1);
+      cfg.blockDim = dim3(gemm_threads(EPI), 1, 1);
       cfg.dynamicSmemBytes = smem;
       int n = 0;
       if (cudaOccupancyMaxActiveClusters(&n, grouped_gemm_pair_kernel<EPI>, &cfg) != cudaSuccess || n <= 0) {
@@ -1337,7 +1392,7 @@ static int run_pair_gemm(const PairProblem& p1, const PairProblem* p2, cudaStrea
   const PairProblem& q = p2 ? *p2 : p1;
   GemmArgs a2 = q.a;
   if (!p2) a2.n_groups = 0;
-  return launch_k(grouped_gemm_pair_kernel<EPI>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kGemmThreads), smem,
+  return launch_k(grouped_gemm_pair_kernel<EPI>, dim3(static_cast<unsigned>(2 * pairs)), dim3(gemm_threads(EPI)), smem,
                   st, p1.ta, p1.tb, p1.ta64, p1.tb64, p1.ta32, p1.ta16, p1.a, q.ta, q.tb, q.ta64, q.tb64, q.ta32,
                   q.ta16, a2, p1.ta32d, p1.ta16d, p1.tb64d, q.ta32d, q.ta16d, q.tb64d) == cudaSuccess ? 0 : -3;
 }
