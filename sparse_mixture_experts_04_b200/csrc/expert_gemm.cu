@@ -145,11 +145,13 @@ struct TileCfg {
 
 // FP32 epilogue staging: one 32 x 32 float block per epilogue warp
 constexpr int kF32StageBytes = 4 * 32 * 32 * 4;
+// 8-bit epilogues: 128 scales per epilogue warp
+constexpr int kI8ScaleBytes = 8 * 128 * 4;
 
 template <int EPI, int BN, int STAGES>
 constexpr int gemm_smem_bytes() {
   return STAGES * TileCfg<EPI, BN>::kStageBytes + 256 /*barriers + flags*/ + 8 * (kMaxGroups + 1) +
-         (EPI == EPI_F32 ? kF32StageBytes + 16 : 0) + 1024 /*alignment slack*/;
+         (EPI == EPI_F32 ? kF32StageBytes + 16 : is_i8(EPI) ? kI8ScaleBytes + 16 : 0) + 1024 /*alignment slack*/;
 }
 
 struct TileInfo {
@@ -259,17 +261,14 @@ __device__ __forceinline__ float i8_silu_mul(uint32_t gi, uint32_t ui, float sa,
   return silu_mul(g, u);
 }
 
-// Eight consecutive outputs of EPI_I8_OUT at element `at`.
-__device__ __forceinline__ void i8_store8(const GemmArgs& args, int64_t at, const float (&v)[8]) {
-  if (args.out_f32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(args.out) + at);
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.out) + at) =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                   pack_bf16x2(v[6], v[7]));
-  }
+// Eight consecutive outputs of EPI_I8_OUT.
+__device__ __forceinline__ void store8(float* out, const float (&v)[8]) {
+  reinterpret_cast<float4*>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* out, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
 // Drain one accumulator (this warp's 32 TMEM lanes, BN columns starting at
@@ -357,28 +356,26 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs& args, int g, int r
 }
 
 // The 8-bit epilogues of one warp: its 32 TMEM lanes, half `half` of the tile's
-// BN columns, whose first is at t_row.  The next block's TMEM load is in flight
-// while one block is scaled and stored.
-template <int BN>
-__device__ __forceinline__ void epilogue_i8_out(const GemmArgs& args, int g, int row, bool row_ok, int n0,
+// BN columns, whose first is at t_row; `cols` of the tile's output columns
+// exist.  The next block's TMEM load is in flight while one block is scaled and
+// stored.  sc: the scales of the warp's B rows in shared memory (i8_tile_scales:
+// BN / 2 of them; SwiGLU: BN / 4 gate scales, then the up scales).
+template <int BN, typename T>
+__device__ __forceinline__ void epilogue_i8_out(T* out, bool row_ok, float sa, const float* sc, int cols,
                                                 uint32_t t_row, int half) {
-  const int64_t at = static_cast<int64_t>(row) * args.ldo + static_cast<int64_t>(g) * args.out_col_stride;
-  const float* bs = args.b_scale + g * args.b_scale_stride;
-  const float sa = row_ok ? args.a_scale[row] : 0.f;
-  const int c0 = half * (BN / 2), c1 = min(c0 + BN / 2, args.N - n0);
+  const int c0 = half * (BN / 2), c1 = min(c0 + BN / 2, cols);
   auto block = [&](const uint32_t (&v)[32], int c) {
     if (!row_ok) return;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int col = n0 + c + q * 8;
-      if (col < args.N) {
-        const float4 s0 = __ldg(reinterpret_cast<const float4*>(bs + col));
-        const float4 s1 = __ldg(reinterpret_cast<const float4*>(bs + col) + 1);
+      if (c + q * 8 < c1) {
+        const float4* sp = reinterpret_cast<const float4*>(sc + (c - c0) + q * 8);
+        const float4 s0 = sp[0], s1 = sp[1];
         const float sb[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
         float y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = __int2float_rn(static_cast<int>(v[q * 8 + j])) * (sa * sb[j]);
-        i8_store8(args, at + col, y);
+        store8(out + c + q * 8, y);
       }
     }
   };
@@ -398,55 +395,84 @@ __device__ __forceinline__ void epilogue_i8_out(const GemmArgs& args, int g, int
   }
 }
 
+// out: the row's FP32 hidden values; returns the bits of the largest magnitude.
 template <int BN>
-__device__ __forceinline__ void epilogue_i8_swiglu(const GemmArgs& args, int g, int row, bool row_ok, int n0,
-                                                   uint32_t t_row, int half) {
-  float* out_row = static_cast<float*>(args.out) + static_cast<int64_t>(row) * args.ldo +
-                   static_cast<int64_t>(g) * args.out_col_stride;
-  const float* bs = args.b_scale + g * args.b_scale_stride;
-  const float sa = row_ok ? args.a_scale[row] : 0.f;
+__device__ __forceinline__ unsigned epilogue_i8_swiglu(float* out, bool row_ok, float sa, const float* sc, int cols,
+                                                       uint32_t t_row, int half) {
   unsigned amax = 0;
-  const int c0 = half * (BN / 4), c1 = min(c0 + BN / 4, args.N - n0);
+  const int c0 = half * (BN / 4), c1 = min(c0 + BN / 4, cols);
   auto block = [&](const uint32_t (&gr)[16], const uint32_t (&ur)[16], int c) {
     if (!row_ok) return;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int col = n0 + c + q * 4;
-      if (col < args.N) {
-        const float4 sg = __ldg(reinterpret_cast<const float4*>(bs + col));
-        const float4 su = __ldg(reinterpret_cast<const float4*>(bs + args.N + col));
+      if (c + q * 4 < c1) {
+        const float4 sg = *reinterpret_cast<const float4*>(sc + (c - c0) + q * 4);
+        const float4 su = *reinterpret_cast<const float4*>(sc + BN / 4 + (c - c0) + q * 4);
         const float h0 = i8_silu_mul(gr[q * 4], ur[q * 4], sa, sg.x, su.x);
         const float h1 = i8_silu_mul(gr[q * 4 + 1], ur[q * 4 + 1], sa, sg.y, su.y);
         const float h2 = i8_silu_mul(gr[q * 4 + 2], ur[q * 4 + 2], sa, sg.z, su.z);
         const float h3 = i8_silu_mul(gr[q * 4 + 3], ur[q * 4 + 3], sa, sg.w, su.w);
         amax = max(max(amax, max(abs_bits(h0), abs_bits(h1))), max(abs_bits(h2), abs_bits(h3)));
-        *reinterpret_cast<float4*>(out_row + col) = make_float4(h0, h1, h2, h3);
+        *reinterpret_cast<float4*>(out + c + q * 4) = make_float4(h0, h1, h2, h3);
       }
     }
   };
-  if (c0 < c1) {
-    uint32_t ga[16], ua[16], gb[16], ub[16];
-    tmem_load_32x16(t_row + c0, ga);
-    tmem_load_32x16(t_row + BN / 2 + c0, ua);
-    tmem_load_wait();
+  if (c0 >= c1) return 0;
+  uint32_t ga[16], ua[16], gb[16], ub[16];
+  tmem_load_32x16(t_row + c0, ga);
+  tmem_load_32x16(t_row + BN / 2 + c0, ua);
+  tmem_load_wait();
 #pragma unroll 1
-    for (int c = c0; c < c1; c += 32) {
-      if (c + 16 < c1) {
-        tmem_load_32x16(t_row + c + 16, gb);
-        tmem_load_32x16(t_row + BN / 2 + c + 16, ub);
-      }
-      block(ga, ua, c);
-      tmem_load_wait();
-      if (c + 16 >= c1) break;
-      if (c + 32 < c1) {
-        tmem_load_32x16(t_row + c + 32, ga);
-        tmem_load_32x16(t_row + BN / 2 + c + 32, ua);
-      }
-      block(gb, ub, c + 16);
-      tmem_load_wait();
+  for (int c = c0; c < c1; c += 32) {
+    if (c + 16 < c1) {
+      tmem_load_32x16(t_row + c + 16, gb);
+      tmem_load_32x16(t_row + BN / 2 + c + 16, ub);
     }
+    block(ga, ua, c);
+    tmem_load_wait();
+    if (c + 16 >= c1) break;
+    if (c + 32 < c1) {
+      tmem_load_32x16(t_row + c + 32, ga);
+      tmem_load_32x16(t_row + BN / 2 + c + 32, ua);
+    }
+    block(gb, ub, c + 16);
+    tmem_load_wait();
   }
-  if (row_ok && amax) atomicMax(args.row_amax + row, amax);
+  return amax;
+}
+
+// The 128 B-row scales of one warp's half of a tile (EPI_I8_OUT: its columns;
+// SwiGLU: 64 gate rows, 64 up rows), a lane's four to sc + 4 lane.
+template <int EPI>
+__device__ __forceinline__ void i8_tile_scales(const GemmArgs& a, const TileInfo& ti, int half, int lane, float* sc) {
+  int col;
+  const float* bs = a.b_scale + ti.g * a.b_scale_stride;
+  if (EPI == EPI_I8_SWIGLU) {
+    col = ti.n0 + half * 64 + (lane & 15) * 4;
+    bs += (lane >> 4) * a.N;
+  } else {
+    col = ti.n0 + half * 128 + lane * 4;
+  }
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (col < a.N) v = __ldg(reinterpret_cast<const float4*>(bs + col));
+  *reinterpret_cast<float4*>(sc + lane * 4) = v;
+}
+
+// Row `row` of a tile through the 8-bit epilogue of EPI.
+template <int EPI, int BN>
+__device__ __forceinline__ void epilogue_i8(const GemmArgs& a, const TileInfo& ti, int row, float sa, const float* sc,
+                                            uint32_t t_row, int half) {
+  const bool ok = row < ti.row_end;
+  const int64_t at = static_cast<int64_t>(row) * a.ldo + static_cast<int64_t>(ti.g) * a.out_col_stride + ti.n0;
+  const int cols = a.N - ti.n0;
+  if constexpr (EPI == EPI_I8_SWIGLU) {
+    const unsigned m = epilogue_i8_swiglu<BN>(static_cast<float*>(a.out) + at, ok, sa, sc, cols, t_row, half);
+    if (ok && m) atomicMax(a.row_amax + row, m);
+  } else if (a.out_f32) {
+    epilogue_i8_out<BN>(static_cast<float*>(a.out) + at, ok, sa, sc, cols, t_row, half);
+  } else {
+    epilogue_i8_out<BN>(static_cast<__nv_bfloat16*>(a.out) + at, ok, sa, sc, cols, t_row, half);
+  }
 }
 
 // FP32 epilogue through shared memory: each 32-column block of this warp's 32
@@ -498,6 +524,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
   int* prefix = reinterpret_cast<int*>(tmem_slot + 4);
   int* prefix2 = prefix + kMaxGroups + 1;
   float* xw_all = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(prefix2 + kMaxGroups + 1) + 15) & ~uintptr_t(15));
+  [[maybe_unused]] float* i8_scales = xw_all;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -655,6 +682,15 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
                                                  C::kOutCols);
       const int acc = it & 1;
       const uint32_t acc_par = static_cast<uint32_t>(it >> 1) & 1u;
+      // 8-bit products: the tile's scales, while its products are computed
+      [[maybe_unused]] float* i8_sc = i8_scales + (warp - 2) * 128;
+      [[maybe_unused]] float sa = 0.f;
+      if constexpr (is_i8(EPI)) {
+        const GemmArgs& A = ti.second ? args2 : args;
+        i8_tile_scales<EPI>(A, ti, (warp - 2) >> 2, lane, i8_sc);
+        if (ti.row0 + r < ti.row_end) sa = __ldg(A.a_scale + ti.row0 + r);
+        __syncwarp();
+      }
       // every lane waits; the result is made warp-uniform (and the warp
       // reconverged) before the .sync.aligned TMEM loads below
       const bool ready = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_par, abort_flag));
@@ -665,10 +701,8 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
       if (EPI == EPI_F32)
         epilogue_f32_staged<BN>(ti.second ? args2 : args, ti.g, ti.row0 + quarter * 32, ti.row_end, t_row, lane,
                                 xw_all + quarter * 32 * 32);
-      else if constexpr (EPI == EPI_I8_SWIGLU)
-        epilogue_i8_swiglu<BN>(ti.second ? args2 : args, ti.g, row, row < ti.row_end, ti.n0, t_row, (warp - 2) >> 2);
-      else if constexpr (EPI == EPI_I8_OUT)
-        epilogue_i8_out<BN>(ti.second ? args2 : args, ti.g, row, row < ti.row_end, ti.n0, t_row, (warp - 2) >> 2);
+      else if constexpr (is_i8(EPI))
+        epilogue_i8<EPI, BN>(ti.second ? args2 : args, ti, row, sa, i8_sc, t_row, (warp - 2) >> 2);
       else
         epilogue_rows<EPI, BN>(ti.second ? args2 : args, ti.g, row, row < ti.row_end, ti.n0, t_row);
       tc_fence_before_sync();
@@ -736,8 +770,9 @@ __device__ __forceinline__ int swap_box_rows(int half_n) {
   return half_n <= 16 ? 16 : half_n <= 32 ? 32 : half_n <= 64 ? 64 : 128;
 }
 
-constexpr int pair_smem_bytes() {
-  return kPairStages * kPairStageBytes + 256 + 8 * (kMaxGroups + 1) + kSwapXBytes + 1024;
+constexpr int pair_smem_bytes(int epi) {
+  return kPairStages * kPairStageBytes + 256 + 8 * (kMaxGroups + 1) + kSwapXBytes + (is_i8(epi) ? kI8ScaleBytes : 0) +
+         1024;
 }
 
 __device__ __forceinline__ TileInfo decode_pair_tile(int tile, int t1, int total, const int* prefix,
@@ -828,7 +863,11 @@ __device__ __forceinline__ void epilogue_swap(const GemmArgs& args, const TileIn
           const float4 s1 = *reinterpret_cast<const float4*>(bs + col + 4);
           const float y[8] = {a.x * (sa * s0.x), a.y * (sa * s0.y), a.z * (sa * s0.z), a.w * (sa * s0.w),
                               b.x * (sa * s1.x), b.y * (sa * s1.y), b.z * (sa * s1.z), b.w * (sa * s1.w)};
-          i8_store8(args, out0 + static_cast<int64_t>(c + j) * args.ldo + col, y);
+          const int64_t at = out0 + static_cast<int64_t>(c + j) * args.ldo + col;
+          if (args.out_f32)
+            store8(static_cast<float*>(args.out) + at, y);
+          else
+            store8(static_cast<__nv_bfloat16*>(args.out) + at, y);
         }
       }
     } else if (EPI == EPI_SWIGLU) {
@@ -912,6 +951,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
   int* prefix = reinterpret_cast<int*>(tmem_slot + 4);
   int* prefix2 = prefix + kMaxGroups + 1;
   float* xbuf = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(prefix2 + kMaxGroups + 1) + 15) & ~uintptr_t(15));
+  [[maybe_unused]] float* i8_scales = xbuf + 32 * kSwapXStride;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -1151,7 +1191,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
       const GemmArgs& A = ti.second ? args2 : args;
       const int acc = it & 1;
       const uint32_t acc_par = static_cast<uint32_t>(it >> 1) & 1u;
-      // all four epilogue warps take the same decision (a swap tile's
+      // 8-bit products: the tile's scales, while its products are computed
+      [[maybe_unused]] float* i8_sc = i8_scales + (warp - 2) * 128;
+      [[maybe_unused]] float sa = 0.f;
+      if constexpr (is_i8(EPI)) {
+        const int row = ti.row0 + 128 * static_cast<int>(rank) + r;
+        if (!ti.swap) i8_tile_scales<EPI>(A, ti, (warp - 2) >> 2, lane, i8_sc);
+        if (!ti.swap && row < ti.row_end) sa = __ldg(A.a_scale + row);
+        __syncwarp();
+      }
+      // all epilogue warps take the same decision (a swap tile's
       // epilogue synchronises them), even when a wait gives up
       const bool ready =
           named_bar_and(2, 32 * epilogue_warps(EPI), mbar_wait(&tfull[acc], acc_par, abort_flag));
@@ -1164,10 +1213,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
         if (half == 0) epilogue_swap<EPI>(A, ti, rank, quarter, lane, (warp - 2) * 32 + lane, t_row, xbuf);
       } else {
         const int row = ti.row0 + 128 * static_cast<int>(rank) + r;
-        if constexpr (EPI == EPI_I8_SWIGLU)
-          epilogue_i8_swiglu<kPairBN>(A, ti.g, row, row < ti.row_end, ti.n0, t_row, half);
-        else if constexpr (EPI == EPI_I8_OUT)
-          epilogue_i8_out<kPairBN>(A, ti.g, row, row < ti.row_end, ti.n0, t_row, half);
+        if constexpr (is_i8(EPI))
+          epilogue_i8<EPI, kPairBN>(A, ti, row, sa, i8_sc, t_row, half);
         else
           epilogue_rows<EPI, kPairBN>(A, ti.g, row, row < ti.row_end, ti.n0, t_row);
       }
@@ -1359,7 +1406,7 @@ struct PairProblem {
 // with p1's (same EPI and tile shape; see decode_pair_tile).
 template <int EPI>
 static int run_pair_gemm(const PairProblem& p1, const PairProblem* p2, cudaStream_t st) {
-  constexpr int smem = pair_smem_bytes();
+  constexpr int smem = pair_smem_bytes(EPI);
   static std::mutex mu;
   static int max_pairs[64] = {0};
   int dev = 0;

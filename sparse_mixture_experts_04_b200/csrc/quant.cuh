@@ -45,21 +45,20 @@ static __device__ __noinline__ float quant_border(float q0, float r, float half)
 __device__ __forceinline__ uint32_t quant_pack4(const float (&v)[4], float scale, float inv) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
   const float half = 0.5f * scale;
-  float q[4], r[4], worst = 0.f;
+  float t[4], r[4], worst = 0.f;  // t: the integer plus kMagic, whose low byte is the integer's
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    q[i] = fmaf(v[i], inv, kMagic) - kMagic;
-    r[i] = fmaf(-q[i], scale, v[i]);
+    t[i] = fmaf(v[i], inv, kMagic);
+    r[i] = fmaf(-(t[i] - kMagic), scale, v[i]);
     worst = fmaxf(worst, fabsf(r[i]));
   }
   if (worst >= half) {  // next to a tie: rare
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (fabsf(r[i]) >= half) q[i] = quant_border(q[i], r[i], half);
+      if (fabsf(r[i]) >= half) t[i] = quant_border(t[i] - kMagic, r[i], half) + kMagic;
   }
-  const uint32_t b0 = __float_as_uint(q[0] + kMagic), b1 = __float_as_uint(q[1] + kMagic);
-  const uint32_t b2 = __float_as_uint(q[2] + kMagic), b3 = __float_as_uint(q[3] + kMagic);
-  const uint32_t w = __byte_perm(__byte_perm(b0, b1, 0x0040), __byte_perm(b2, b3, 0x0040), 0x5410);
+  const uint32_t w = __byte_perm(__byte_perm(__float_as_uint(t[0]), __float_as_uint(t[1]), 0x0040),
+                                 __byte_perm(__float_as_uint(t[2]), __float_as_uint(t[3]), 0x0040), 0x5410);
   return scale == scale ? w : 0u;
 }
 
