@@ -260,40 +260,36 @@ def moe_ep_plan(n_ranks: int, rank: int, n_experts: int, seg_off_all) -> tuple:
 
 
 # ------------------------------------------------- few tokens and 8-bit integers
-def _need(name: str, t: torch.Tensor, shape, dtype, device) -> None:
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+def _need(name: str, t: torch.Tensor, shape, dtype, dev: int) -> None:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _need_ws(ws: torch.Tensor, device) -> None:
-    if ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise ValueError(f"the workspace must be a contiguous uint8 tensor on {device}")
+def _need_ws(ws: torch.Tensor, dev: int) -> None:
+    if ws.get_device() != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous uint8 tensor on cuda:{dev}")
 
 
-def _cuda(name: str, t: torch.Tensor) -> torch.device:
+def _cuda(name: str, t: torch.Tensor) -> int:
+    """The index of the CUDA device t is on."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
-    return t.device
+    return t.get_device()
 
 
-class _on:
-    """Makes `device` current for a call (its launches and attributes are the
-    current device's) and gives the stream handle: `stream`, or that device's
-    current stream."""
-
-    def __init__(self, device: torch.device, stream):
-        self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
-        self.device, self.stream = device, stream
-
-    def __enter__(self) -> int:
-        if self.guard is not None:
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream if self.stream is None else _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _enqueue(name: str, dev: int, stream, *args) -> None:
+    """Call the C entry point `name` with args and the stream handle (`stream`,
+    or device dev's current stream), device dev being current."""
+    fn = getattr(_lib.lib(), name)
+    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, st)
+    _lib.check(name, rc)
 
 
 _ACT_DTYPE = {DTYPE_BF16: torch.bfloat16, DTYPE_F32: torch.float32}
@@ -338,10 +334,8 @@ def _layer_call(name: str, prob, x, w_struct, y, routing, stats, ws, stream):
     _need("y", y, shape, dt, dev)
     _need_ws(ws, dev)
     r = _routing_struct(routing)
-    with _on(dev, stream) as st:
-        rc = getattr(_lib.lib(), name)(ctypes.byref(prob), _p(x), ctypes.byref(w_struct), _p(y),
-                                       ctypes.byref(r) if r is not None else None, _p(stats), _p(ws), ws.numel(), st)
-    _lib.check(name, rc)
+    _enqueue(name, dev, stream, ctypes.byref(prob), x.data_ptr(), ctypes.byref(w_struct), y.data_ptr(),
+             ctypes.byref(r) if r is not None else None, _p(stats), ws.data_ptr(), ws.numel())
 
 
 def moe_layer_forward_few(prob, x, weights: dict, y, routing: dict | None, stats, ws, stream=None):
@@ -373,10 +367,8 @@ def moe_quantize_rows(x, x_q, x_scale, stream=None):
     _need("x_q", x_q, x.shape, torch.int8, dev)
     _need("x_scale", x_scale, x.shape[:-1], torch.float32, dev)
     n = x.shape[-1]
-    with _on(dev, stream) as st:
-        rc = _lib.lib().moe_quantize_rows(x.numel() // n if n else 0, n, _ACT_CODE[x.dtype], _p(x), _p(x_q),
-                                          _p(x_scale), st)
-    _lib.check("moe_quantize_rows", rc)
+    _enqueue("moe_quantize_rows", dev, stream, x.numel() // n if n else 0, n, _ACT_CODE[x.dtype], x.data_ptr(),
+             x_q.data_ptr(), x_scale.data_ptr())
 
 
 def quantize_rows(x: torch.Tensor, stream=None) -> tuple:
@@ -393,25 +385,23 @@ def moe_matmul_i8(x_q, x_scale, seg_off, w, w_scale, y, ws, stream=None):
     and [N] with seg_off None: every row); y [n_rows, N] BF16 or FP32; ws from
     alloc_matmul_workspace."""
     dev = _cuda("x_q", x_q)
-    if w.dim() not in (2, 3) or x_q.dim() != 2:
+    wshape = w.shape
+    if len(wshape) not in (2, 3) or x_q.dim() != 2:
         raise ValueError("x_q must be [n_rows, K] and w [G, N, K] or [N, K]")
-    G = w.shape[0] if w.dim() == 3 else 1
-    N, K = w.shape[-2], w.shape[-1]
-    rows = x_q.shape[0]
-    if y.dtype not in _ACT_CODE:
+    G, N, K = wshape if len(wshape) == 3 else (1, *wshape)
+    rows, out = len(x_q), _ACT_CODE.get(y.dtype)
+    if out is None:
         raise ValueError(f"y must be BF16 or FP32, got {y.dtype}")
     _need("x_q", x_q, (rows, K), torch.int8, dev)
     _need("x_scale", x_scale, (rows,), torch.float32, dev)
-    _need("w", w, w.shape, torch.int8, dev)
-    _need("w_scale", w_scale, w.shape[:-1], torch.float32, dev)
+    _need("w", w, wshape, torch.int8, dev)
+    _need("w_scale", w_scale, wshape[:-1], torch.float32, dev)
     _need("y", y, (rows, N), y.dtype, dev)
     _need_ws(ws, dev)
     if seg_off is not None:
         _need("seg_off", seg_off, (G + 1,), torch.int32, dev)
-    with _on(dev, stream) as st:
-        rc = _lib.lib().moe_matmul_i8(G, rows, N, K, _p(x_q), _p(x_scale), _p(seg_off), _p(w), _p(w_scale),
-                                      _ACT_CODE[y.dtype], _p(y), _p(ws), ws.numel(), st)
-    _lib.check("moe_matmul_i8", rc)
+    _enqueue("moe_matmul_i8", dev, stream, G, rows, N, K, x_q.data_ptr(), x_scale.data_ptr(), _p(seg_off),
+             w.data_ptr(), w_scale.data_ptr(), out, y.data_ptr(), ws.data_ptr(), ws.numel())
 
 
 def moe_expert_ffn_i8(prob, mode, x_q, x_scale, seg_off, w13, w13_scale, w2, w2_scale, y_rows, ws, stream=None):
@@ -433,11 +423,9 @@ def moe_expert_ffn_i8(prob, mode, x_q, x_scale, seg_off, w13, w13_scale, w2, w2_
     _need_ws(ws, dev)
     if mode != FFN_SHARED and seg_off is not None:
         _need("seg_off", seg_off, (G + 1,), torch.int32, dev)
-    with _on(dev, stream) as st:
-        rc = _lib.lib().moe_expert_ffn_i8(ctypes.byref(prob), int(mode), _p(x_q), _p(x_scale), rows, _p(seg_off),
-                                          _p(w13), _p(w13_scale), _p(w2), _p(w2_scale), _p(y_rows), _p(ws),
-                                          ws.numel(), st)
-    _lib.check("moe_expert_ffn_i8", rc)
+    _enqueue("moe_expert_ffn_i8", dev, stream, ctypes.byref(prob), int(mode), x_q.data_ptr(), x_scale.data_ptr(),
+             rows, _p(seg_off), w13.data_ptr(), w13_scale.data_ptr(), w2.data_ptr(), w2_scale.data_ptr(),
+             y_rows.data_ptr(), ws.data_ptr(), ws.numel())
 
 
 # ----------------------------------------------------- expert parallel over peer memory

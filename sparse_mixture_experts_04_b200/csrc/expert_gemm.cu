@@ -441,17 +441,18 @@ __device__ __forceinline__ unsigned epilogue_i8_swiglu(float* out, bool row_ok, 
   return amax;
 }
 
-// The 128 B-row scales of one warp's half of a tile (EPI_I8_OUT: its columns;
-// SwiGLU: 64 gate rows, 64 up rows), a lane's four to sc + 4 lane.
-template <int EPI>
+// The BN / 2 B-row scales of one warp's half of a tile (EPI_I8_OUT: its columns;
+// SwiGLU: BN / 4 gate rows, then the up rows), a lane's four to sc + 4 lane.
+template <int EPI, int BN>
 __device__ __forceinline__ void i8_tile_scales(const GemmArgs& a, const TileInfo& ti, int half, int lane, float* sc) {
+  if (lane >= BN / 8) return;
   int col;
   const float* bs = a.b_scale + ti.g * a.b_scale_stride;
   if (EPI == EPI_I8_SWIGLU) {
-    col = ti.n0 + half * 64 + (lane & 15) * 4;
-    bs += (lane >> 4) * a.N;
+    col = ti.n0 + half * (BN / 4) + (lane % (BN / 16)) * 4;
+    bs += (lane / (BN / 16)) * a.N;
   } else {
-    col = ti.n0 + half * 128 + lane * 4;
+    col = ti.n0 + half * (BN / 2) + lane * 4;
   }
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < a.N) v = __ldg(reinterpret_cast<const float4*>(bs + col));
@@ -687,7 +688,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
       [[maybe_unused]] float sa = 0.f;
       if constexpr (is_i8(EPI)) {
         const GemmArgs& A = ti.second ? args2 : args;
-        i8_tile_scales<EPI>(A, ti, (warp - 2) >> 2, lane, i8_sc);
+        i8_tile_scales<EPI, BN>(A, ti, (warp - 2) >> 2, lane, i8_sc);
         if (ti.row0 + r < ti.row_end) sa = __ldg(A.a_scale + ti.row0 + r);
         __syncwarp();
       }
@@ -1196,7 +1197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
       [[maybe_unused]] float sa = 0.f;
       if constexpr (is_i8(EPI)) {
         const int row = ti.row0 + 128 * static_cast<int>(rank) + r;
-        if (!ti.swap) i8_tile_scales<EPI>(A, ti, (warp - 2) >> 2, lane, i8_sc);
+        if (!ti.swap) i8_tile_scales<EPI, kPairBN>(A, ti, (warp - 2) >> 2, lane, i8_sc);
         if (!ti.swap && row < ti.row_end) sa = __ldg(A.a_scale + row);
         __syncwarp();
       }
@@ -2040,18 +2041,19 @@ static bool i8_pair_problem(const I8Gemm& g, bool swiglu, PairProblem* q) {
   return true;
 }
 
-static bool i8_single_problem(const I8Gemm& g, bool swiglu, SingleProblem* q) {
+// bn: B rows of a tile (SwiGLU: half of them gate rows, half up rows).
+static bool i8_single_problem(const I8Gemm& g, bool swiglu, int bn, SingleProblem* q) {
   const uint64_t K = static_cast<uint64_t>(g.K / 2);
   const uint64_t da[2] = {K * g.k_groups, static_cast<uint64_t>(g.n_rows)};
   const uint32_t ba[2] = {kBK, kBM};
   const uint64_t db[3] = {K, static_cast<uint64_t>(g.N),
                           static_cast<uint64_t>(g.n_groups) * (swiglu ? 2 : g.k_groups)};
-  const uint32_t bb[3] = {kBK, static_cast<uint32_t>(swiglu ? 128 : 256), 1};
+  const uint32_t bb[3] = {kBK, static_cast<uint32_t>(swiglu ? bn / 2 : bn), 1};
   if (!make_map(&q->ta, g.a, 2, da, ba) || !make_map(&q->tb, g.w, 3, db, bb)) return false;
   i8_args(g, &q->a);
   q->a.stall_ns = test_stall_ns();
   const int64_t mt = g.seg_off ? cdiv(g.n_rows, kBM) + g.n_groups : g.n_groups * cdiv(g.n_rows, kBM);
-  q->tile_bound = mt * cdiv(g.N, swiglu ? 128 : 256);
+  q->tile_bound = mt * cdiv(g.N, swiglu ? bn / 2 : bn);
   return true;
 }
 
@@ -2069,8 +2071,16 @@ static int run_i8(const I8Gemm& g, cudaStream_t st) {
     if (!i8_pair_problem(g, EPI == EPI_I8_SWIGLU, &q)) return -3;
     return run_pair_gemm<EPI>(q, nullptr, st);
   }
+  // 256 B rows per tile, or 64 where 256 would leave SMs without a tile (one row,
+  // K = 2048, N = 2816: 11 tiles 9.9 us, 44 tiles I8_ONE_US us)
+  constexpr bool kSwiglu = EPI == EPI_I8_SWIGLU;
+  const int64_t blocks = cdiv(g.n_rows, kBM) + (g.n_groups < g.n_rows ? g.n_groups : g.n_rows) - 1;
   SingleProblem q;
-  if (!i8_single_problem(g, EPI == EPI_I8_SWIGLU, &q)) return -3;
+  if (blocks * cdiv(g.N, kSwiglu ? 128 : 256) < num_sms()) {
+    if (!i8_single_problem(g, kSwiglu, 64, &q)) return -3;
+    return run_gemm<EPI, 64, 8>(q.ta, q.tb, q.a, q.tile_bound, st);
+  }
+  if (!i8_single_problem(g, kSwiglu, 256, &q)) return -3;
   return run_gemm<EPI, 256, 4>(q.ta, q.tb, q.a, q.tile_bound, st);
 }
 

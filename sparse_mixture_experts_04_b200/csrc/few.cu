@@ -541,45 +541,46 @@ __device__ __forceinline__ void few_load_tokens(const Few<WT>& f, int pass, cons
   const FewArgs& a = f.a;
   const bool up = pass <= kUpRouted;
   const bool routed = pass == kUpRouted || pass == kDownRouted;
-  const int vecs = q.len / 16, all = ((q.len + 63) & ~63) / 16, total = q.n * all;
+  const int vecs = q.len / 16, all = ((q.len + 63) & ~63) / 16;
+  // 256 / (n rounded up to a power of two) threads per row
+  const int sh = __clz(q.n - 1) - 24;
+  const int per = 1 << sh, r = tid >> sh, v0 = tid & (per - 1);
   if (WT != kFewI8 || up) {
-    const char* base = static_cast<const char*>(up ? (WT == kFewI8 ? static_cast<const void*>(a.x_q) : a.x)
-                                                   : (routed ? a.h : a.h_s));
-    for (int i0 = tid; i0 < total; i0 += 4 * kFewWorkers) {
-      uint4 z[4];
+    if (r < q.n) {
+      const char* src;
+      if (up)
+        src = static_cast<const char*>(WT == kFewI8 ? static_cast<const void*>(a.x_q) : a.x) +
+              static_cast<int64_t>(routed ? f.s.perm[q.row0 + r] / a.K : q.row0 + r) * q.len;
+      else
+        src = static_cast<const char*>(routed ? a.h : a.h_s) +
+              (routed ? q.row0 + r : static_cast<int64_t>(q.row0 + r) * a.Ns + q.e) * a.F * Few<WT>::kW +
+              static_cast<int64_t>(q.c) * a.chunk_bytes;
+      uint8_t* dst = f.tok + r * t_pitch;
+      for (int v = v0; v < all; v += 4 * per) {
+        uint4 z[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + j * kFewWorkers, r = i / all, v = i - r * all;
-        z[j] = make_uint4(0, 0, 0, 0);
-        if (i < total && v < vecs) {
-          int64_t at;
-          if (up)
-            at = static_cast<int64_t>(routed ? f.s.perm[q.row0 + r] / a.K : q.row0 + r) * q.len;
-          else
-            at = (routed ? q.row0 + r : static_cast<int64_t>(q.row0 + r) * a.Ns + q.e) * a.F * Few<WT>::kW +
-                 static_cast<int64_t>(q.c) * a.chunk_bytes;
-          z[j] = __ldcg(reinterpret_cast<const uint4*>(base + at) + v);
+        for (int j = 0; j < 4; ++j) {
+          z[j] = make_uint4(0, 0, 0, 0);
+          if (v + j * per < vecs) z[j] = __ldcg(reinterpret_cast<const uint4*>(src) + v + j * per);
         }
-      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + j * kFewWorkers, r = i / all, v = i - r * all;
-        if (i < total) *reinterpret_cast<uint4*>(f.tok + r * t_pitch + v * 16) = z[j];
+        for (int j = 0; j < 4; ++j)
+          if (v + j * per < all) *reinterpret_cast<uint4*>(dst + (v + j * per) * 16) = z[j];
       }
     }
     if (WT == kFewI8 && tid < q.n)
       f.s.row_scale[tid] = __ldcg(a.x_scale + (routed ? f.s.perm[q.row0 + tid] / a.K : q.row0 + tid));
   } else {
-    for (int i = tid; i < total; i += kFewWorkers) {
-      const int r = i / all, v = i - r * all;
-      const int64_t row = q.row0 + r;
+    if (r >= q.n) return;
+    const int64_t row = q.row0 + r;
+    const unsigned m = __ldcg(a.amax + (routed ? row : static_cast<int64_t>(a.T) * a.K + row));
+    for (int v = v0; v < all; v += per) {
       const float4* src = reinterpret_cast<const float4*>(
           (routed ? static_cast<const float*>(a.h) + row * a.F
                   : static_cast<const float*>(a.h_s) + (row * a.Ns + q.e) * a.F) +
           static_cast<int64_t>(q.c) * a.chunk_bytes) + v * 4;
       uint32_t w[4] = {0, 0, 0, 0};
       float4 z[4];
-      const unsigned m = __ldcg(a.amax + (routed ? row : static_cast<int64_t>(a.T) * a.K + row));
       if (v < vecs) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[j] = __ldcg(src + j);

@@ -107,18 +107,29 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const T* _
   }
 }
 
-// One warp per row, for many rows that fit its registers: the row stays packed
-// between the maximum and the rounding, with all its loads in flight and no
-// block barrier.  A block per row took 150 us for 65536 rows of 2048 BF16 (two
-// barriers and a mostly idle block per 4 KB), a warp per row 62 us: 402 MB,
-// the HBM rate.
-// kVecs: 16-byte vectors a lane keeps; 8 leave room for twice the warps of 16.
+// One warp per row, for many rows: all loads of a chunk (8 vectors of 16 bytes
+// per lane) in flight and no block barrier.  A row of one chunk stays packed in
+// registers between the maximum and the rounding; longer ones are read again,
+// from L2.  (A block per row took 150 us for 65536 rows of 2048 BF16: two
+// barriers and a mostly idle block per 4 KB.  A warp per row: 74 us, 402 MB.)
+constexpr int kQuantVecs = 8;
 
-template <typename T, int kVecs>
-__global__ void __launch_bounds__(kQuantThreads, kVecs <= 8 ? 4 : 2) quantize_rows_warp_kernel(const T* __restrict__ x, int64_t n_rows,
-                                                                           int n_cols, int8_t* __restrict__ q,
-                                                                           float* __restrict__ scale) {
+template <typename T>
+__device__ __forceinline__ void load_chunk(const uint4* xr, int first, int vecs, int lane, uint4 (&v)[kQuantVecs]) {
+#pragma unroll
+  for (int i = 0; i < kQuantVecs; ++i) {
+    const int at = first + lane + i * 32;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (at < vecs) v[i] = __ldg(xr + at);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads, 4) quantize_rows_warp_kernel(const T* __restrict__ x, int64_t n_rows,
+                                                                              int n_cols, int8_t* __restrict__ q,
+                                                                              float* __restrict__ scale) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));  // elements of a vector
+  constexpr int kChunk = 32 * kQuantVecs;              // vectors of a chunk
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, vecs = n_cols / V;
@@ -126,40 +137,44 @@ __global__ void __launch_bounds__(kQuantThreads, kVecs <= 8 ? 4 : 2) quantize_ro
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5); row < n_rows;
        row += warps) {
     const uint4* xr = reinterpret_cast<const uint4*>(x + row * n_cols);
-    uint4 v[kVecs];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (lane + i * 32 < vecs) v[i] = __ldcs(xr + lane + i * 32);
-    }
+    uint4 v[kQuantVecs];
     unsigned m = 0;
+#pragma unroll 1
+    for (int first = 0; first < vecs; first += kChunk) {
+      load_chunk<T>(xr, first, vecs, lane, v);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      for (int i = 0; i < kQuantVecs; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (sizeof(T) == 2)  // the magnitudes' bits of two BF16 order as 16-bit integers
-          m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
-        else
-          m = max(m, w[j] & 0x7FFFFFFFu);
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (sizeof(T) == 2)  // the magnitudes' bits of two BF16 order as 16-bit integers
+            m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+          else
+            m = max(m, w[j] & 0x7FFFFFFFu);
+        }
       }
     }
     if constexpr (sizeof(T) == 2) m = max(m & 0xFFFF0000u, m << 16);
     const float s = quant_scale(warp_max_u32(m));
     const float inv = 1.0f / s;
     int8_t* qr = q + row * n_cols;
+#pragma unroll 1
+    for (int first = 0; first < vecs; first += kChunk) {
+      if (vecs > kChunk) load_chunk<T>(xr, first, vecs, lane, v);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      if (lane + i * 32 < vecs) {
-        if constexpr (sizeof(T) == 2) {
-          const float lo[4] = {bf16_lo(v[i].x), bf16_hi(v[i].x), bf16_lo(v[i].y), bf16_hi(v[i].y)};
-          const float hi[4] = {bf16_lo(v[i].z), bf16_hi(v[i].z), bf16_lo(v[i].w), bf16_hi(v[i].w)};
-          *reinterpret_cast<uint2*>(qr + (lane + i * 32) * 8) =
-              make_uint2(quant_pack4(lo, s, inv), quant_pack4(hi, s, inv));
-        } else {
-          const float f[4] = {__uint_as_float(v[i].x), __uint_as_float(v[i].y), __uint_as_float(v[i].z),
-                              __uint_as_float(v[i].w)};
-          *reinterpret_cast<uint32_t*>(qr + (lane + i * 32) * 4) = quant_pack4(f, s, inv);
+      for (int i = 0; i < kQuantVecs; ++i) {
+        const int at = first + lane + i * 32;
+        if (at < vecs) {
+          if constexpr (sizeof(T) == 2) {
+            const float lo[4] = {bf16_lo(v[i].x), bf16_hi(v[i].x), bf16_lo(v[i].y), bf16_hi(v[i].y)};
+            const float hi[4] = {bf16_lo(v[i].z), bf16_hi(v[i].z), bf16_lo(v[i].w), bf16_hi(v[i].w)};
+            *reinterpret_cast<uint2*>(qr + static_cast<int64_t>(at) * 8) =
+                make_uint2(quant_pack4(lo, s, inv), quant_pack4(hi, s, inv));
+          } else {
+            const float f[4] = {__uint_as_float(v[i].x), __uint_as_float(v[i].y), __uint_as_float(v[i].z),
+                                __uint_as_float(v[i].w)};
+            *reinterpret_cast<uint32_t*>(qr + static_cast<int64_t>(at) * 4) = quant_pack4(f, s, inv);
+          }
         }
       }
     }
@@ -170,17 +185,14 @@ __global__ void __launch_bounds__(kQuantThreads, kVecs <= 8 ? 4 : 2) quantize_ro
 template <typename T>
 static cudaError_t run_quantize_rows(const T* x, int64_t n_rows, int n_cols, int8_t* q, float* scale,
                                      cudaStream_t st) {
-  // a warp per row once the rows give every SM a few warps; fewer or longer
-  // rows take a block each (one row of 2048: the block's 128 threads load it at
-  // once, a warp would need four rounds)
-  constexpr int kPerVec = 32 * 16 / static_cast<int>(sizeof(T));  // elements of one vector per lane
-  if (n_rows >= 4 * num_sms() && n_cols <= 16 * kPerVec) {
+  // a warp per row once the rows give every SM a few warps, for rows of several
+  // chunks many warps (600 rows of 8192: 37 us so, 13 us a block each); else a
+  // block per row
+  const bool one_chunk = n_cols <= kQuantVecs * 32 * 16 / static_cast<int>(sizeof(T));
+  if ((one_chunk && n_rows >= 4 * num_sms()) || (n_cols <= 8192 && n_rows >= 48 * num_sms())) {
     int64_t grid = (n_rows + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
     if (grid > 65536) grid = 65536;
-    if (n_cols <= 8 * kPerVec)
-      return launch_k(quantize_rows_warp_kernel<T, 8>, dim3(static_cast<unsigned>(grid)), dim3(kQuantThreads), 0, st, x,
-                      n_rows, n_cols, q, scale);
-    return launch_k(quantize_rows_warp_kernel<T, 16>, dim3(static_cast<unsigned>(grid)), dim3(kQuantThreads), 0, st, x,
+    return launch_k(quantize_rows_warp_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(kQuantThreads), 0, st, x,
                     n_rows, n_cols, q, scale);
   }
   const unsigned grid = static_cast<unsigned>(n_rows < 65536 ? n_rows : 65536);
