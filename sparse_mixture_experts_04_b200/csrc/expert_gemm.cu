@@ -145,13 +145,14 @@ struct TileCfg {
 
 // FP32 epilogue staging: one 32 x 32 float block per epilogue warp
 constexpr int kF32StageBytes = 4 * 32 * 32 * 4;
-// 8-bit epilogues: 128 scales per epilogue warp
+// 8-bit epilogues: 128 scales per epilogue warp; single CTAs: 2 KB of staging each
 constexpr int kI8ScaleBytes = 8 * 128 * 4;
+constexpr int kI8StageBytes = 8 * 2048;
 
 template <int EPI, int BN, int STAGES>
 constexpr int gemm_smem_bytes() {
   return STAGES * TileCfg<EPI, BN>::kStageBytes + 256 /*barriers + flags*/ + 8 * (kMaxGroups + 1) +
-         (EPI == EPI_F32 ? kF32StageBytes + 16 : is_i8(EPI) ? kI8ScaleBytes + 16 : 0) + 1024 /*alignment slack*/;
+         (EPI == EPI_F32 ? kF32StageBytes + 16 : is_i8(EPI) ? kI8ScaleBytes + kI8StageBytes + 16 : 0) + 1024 /*alignment slack*/;
 }
 
 struct TileInfo {
@@ -355,27 +356,62 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs& args, int g, int r
   }
 }
 
+// 64 bytes of each of a warp's 32 rows to global memory through shared memory
+// (buf: 2 KB): lane l holds row l's four 16-byte pieces; after the exchange four
+// lanes write one row's 64 bytes, so a store instruction touches 8 rows instead
+// of 32.  (Stored row per lane, the stores' 32 lines per instruction took most
+// of the epilogue: 11300 cycles for a 256 x 256 BF16 tile.)  rows: the warp's
+// rows that exist; pieces: those of the 64 bytes that do; stride in bytes.
+__device__ __forceinline__ void store_rows64(char* out, int64_t stride, int rows, int pieces, const uint4 (&v)[4],
+                                             uint4* buf, int lane) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) buf[lane * 4 + (p ^ ((lane >> 1) & 3))] = v[p];
+  __syncwarp();
+  const int p = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    const uint4 w = buf[r * 4 + (p ^ ((r >> 1) & 3))];
+    if (r < rows && p < pieces) *reinterpret_cast<uint4*>(out + r * stride + p * 16) = w;
+  }
+  __syncwarp();
+}
+
 // The 8-bit epilogues of one warp: its 32 TMEM lanes, half `half` of the tile's
-// BN columns, whose first is at t_row; `cols` of the tile's output columns
-// exist.  The next block's TMEM load is in flight while one block is scaled and
+// BN columns, whose first is at t_row; `cols` of the tile's output columns and
+// `rows` of the warp's rows exist; out: the warp's first row, ldo elements
+// apart.  The next block's TMEM load is in flight while one block is scaled and
 // stored.  sc: the scales of the warp's B rows in shared memory (i8_tile_scales:
 // BN / 2 of them; SwiGLU: BN / 4 gate scales, then the up scales).
 template <int BN, typename T>
-__device__ __forceinline__ void epilogue_i8_out(T* out, bool row_ok, float sa, const float* sc, int cols,
-                                                uint32_t t_row, int half) {
+__device__ __forceinline__ void epilogue_i8_out(T* out, int64_t ldo, int rows, float sa, const float* sc, int cols,
+                                                uint32_t t_row, int half, uint4* buf, int lane) {
   const int c0 = half * (BN / 2), c1 = min(c0 + BN / 2, cols);
   auto block = [&](const uint32_t (&v)[32], int c) {
-    if (!row_ok) return;
+    const float4* sp = reinterpret_cast<const float4*>(sc + (c - c0));
+    uint4 w[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (c + q * 8 < c1) {
-        const float4* sp = reinterpret_cast<const float4*>(sc + (c - c0) + q * 8);
-        const float4 s0 = sp[0], s1 = sp[1];
-        const float sb[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = __int2float_rn(static_cast<int>(v[q * 8 + j])) * (sa * sb[j]);
-        store8(out + c + q * 8, y);
+    for (int q = 0; q < 8; ++q) {
+      const float4 s = sp[q];
+      const float y0 = __int2float_rn(static_cast<int>(v[q * 4])) * (sa * s.x);
+      const float y1 = __int2float_rn(static_cast<int>(v[q * 4 + 1])) * (sa * s.y);
+      const float y2 = __int2float_rn(static_cast<int>(v[q * 4 + 2])) * (sa * s.z);
+      const float y3 = __int2float_rn(static_cast<int>(v[q * 4 + 3])) * (sa * s.w);
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t lo = pack_bf16x2(y0, y1), hi = pack_bf16x2(y2, y3);
+        if (q & 1) {
+          w[q >> 1].z = lo;
+          w[q >> 1].w = hi;
+        } else {
+          w[q >> 1].x = lo;
+          w[q >> 1].y = hi;
+        }
+        if (q == 7) store_rows64(reinterpret_cast<char*>(out + c), ldo * 2, rows, (c1 - c) / 8, w, buf, lane);
+      } else {
+        w[q & 3] = make_uint4(__float_as_uint(y0), __float_as_uint(y1), __float_as_uint(y2), __float_as_uint(y3));
+        if ((q & 3) == 3)
+          store_rows64(reinterpret_cast<char*>(out + c + (q >> 2) * 16), ldo * 4, rows, (c1 - c) / 4 - (q >> 2) * 4, w,
+                       buf, lane);
       }
     }
   };
@@ -395,27 +431,27 @@ __device__ __forceinline__ void epilogue_i8_out(T* out, bool row_ok, float sa, c
   }
 }
 
-// out: the row's FP32 hidden values; returns the bits of the largest magnitude.
+// out: FP32 hidden rows; returns the bits of the largest magnitude of the
+// lane's row (columns past `cols` have zero products, so they do not count).
 template <int BN>
-__device__ __forceinline__ unsigned epilogue_i8_swiglu(float* out, bool row_ok, float sa, const float* sc, int cols,
-                                                       uint32_t t_row, int half) {
+__device__ __forceinline__ unsigned epilogue_i8_swiglu(float* out, int64_t ldo, int rows, float sa, const float* sc,
+                                                       int cols, uint32_t t_row, int half, uint4* buf, int lane) {
   unsigned amax = 0;
   const int c0 = half * (BN / 4), c1 = min(c0 + BN / 4, cols);
   auto block = [&](const uint32_t (&gr)[16], const uint32_t (&ur)[16], int c) {
-    if (!row_ok) return;
+    uint4 w[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (c + q * 4 < c1) {
-        const float4 sg = *reinterpret_cast<const float4*>(sc + (c - c0) + q * 4);
-        const float4 su = *reinterpret_cast<const float4*>(sc + BN / 4 + (c - c0) + q * 4);
-        const float h0 = i8_silu_mul(gr[q * 4], ur[q * 4], sa, sg.x, su.x);
-        const float h1 = i8_silu_mul(gr[q * 4 + 1], ur[q * 4 + 1], sa, sg.y, su.y);
-        const float h2 = i8_silu_mul(gr[q * 4 + 2], ur[q * 4 + 2], sa, sg.z, su.z);
-        const float h3 = i8_silu_mul(gr[q * 4 + 3], ur[q * 4 + 3], sa, sg.w, su.w);
-        amax = max(max(amax, max(abs_bits(h0), abs_bits(h1))), max(abs_bits(h2), abs_bits(h3)));
-        *reinterpret_cast<float4*>(out + c + q * 4) = make_float4(h0, h1, h2, h3);
-      }
+      const float4 sg = *reinterpret_cast<const float4*>(sc + (c - c0) + q * 4);
+      const float4 su = *reinterpret_cast<const float4*>(sc + BN / 4 + (c - c0) + q * 4);
+      const float h0 = i8_silu_mul(gr[q * 4], ur[q * 4], sa, sg.x, su.x);
+      const float h1 = i8_silu_mul(gr[q * 4 + 1], ur[q * 4 + 1], sa, sg.y, su.y);
+      const float h2 = i8_silu_mul(gr[q * 4 + 2], ur[q * 4 + 2], sa, sg.z, su.z);
+      const float h3 = i8_silu_mul(gr[q * 4 + 3], ur[q * 4 + 3], sa, sg.w, su.w);
+      amax = max(max(amax, max(abs_bits(h0), abs_bits(h1))), max(abs_bits(h2), abs_bits(h3)));
+      w[q] = make_uint4(__float_as_uint(h0), __float_as_uint(h1), __float_as_uint(h2), __float_as_uint(h3));
     }
+    store_rows64(reinterpret_cast<char*>(out + c), ldo * 4, rows, (c1 - c) / 4, w, buf, lane);
   };
   if (c0 >= c1) return 0;
   uint32_t ga[16], ua[16], gb[16], ub[16];
@@ -459,20 +495,22 @@ __device__ __forceinline__ void i8_tile_scales(const GemmArgs& a, const TileInfo
   *reinterpret_cast<float4*>(sc + lane * 4) = v;
 }
 
-// Row `row` of a tile through the 8-bit epilogue of EPI.
+// A warp's rows row0 .. row0 + 31 of a tile (lane: its row) through the 8-bit
+// epilogue of EPI.  sa: the scale of the lane's row (0 past the last row).
 template <int EPI, int BN>
-__device__ __forceinline__ void epilogue_i8(const GemmArgs& a, const TileInfo& ti, int row, float sa, const float* sc,
-                                            uint32_t t_row, int half) {
-  const bool ok = row < ti.row_end;
-  const int64_t at = static_cast<int64_t>(row) * a.ldo + static_cast<int64_t>(ti.g) * a.out_col_stride + ti.n0;
-  const int cols = a.N - ti.n0;
+__device__ __forceinline__ void epilogue_i8(const GemmArgs& a, const TileInfo& ti, int row0, float sa, const float* sc,
+                                            uint32_t t_row, int half, uint4* buf, int lane) {
+  const int64_t at = static_cast<int64_t>(row0) * a.ldo + static_cast<int64_t>(ti.g) * a.out_col_stride + ti.n0;
+  const int cols = a.N - ti.n0, rows = ti.row_end - row0;
+  if (rows <= 0) return;
   if constexpr (EPI == EPI_I8_SWIGLU) {
-    const unsigned m = epilogue_i8_swiglu<BN>(static_cast<float*>(a.out) + at, ok, sa, sc, cols, t_row, half);
-    if (ok && m) atomicMax(a.row_amax + row, m);
+    const unsigned m =
+        epilogue_i8_swiglu<BN>(static_cast<float*>(a.out) + at, a.ldo, rows, sa, sc, cols, t_row, half, buf, lane);
+    if (lane < rows && m) atomicMax(a.row_amax + row0 + lane, m);
   } else if (a.out_f32) {
-    epilogue_i8_out<BN>(static_cast<float*>(a.out) + at, ok, sa, sc, cols, t_row, half);
+    epilogue_i8_out<BN>(static_cast<float*>(a.out) + at, a.ldo, rows, sa, sc, cols, t_row, half, buf, lane);
   } else {
-    epilogue_i8_out<BN>(static_cast<__nv_bfloat16*>(a.out) + at, ok, sa, sc, cols, t_row, half);
+    epilogue_i8_out<BN>(static_cast<__nv_bfloat16*>(a.out) + at, a.ldo, rows, sa, sc, cols, t_row, half, buf, lane);
   }
 }
 
@@ -525,7 +563,8 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
   int* prefix = reinterpret_cast<int*>(tmem_slot + 4);
   int* prefix2 = prefix + kMaxGroups + 1;
   float* xw_all = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(prefix2 + kMaxGroups + 1) + 15) & ~uintptr_t(15));
-  [[maybe_unused]] float* i8_scales = xw_all;
+  [[maybe_unused]] float* i8_scales = xw_all;  // 8-bit epilogues: 128 scales, then 2 KB per warp
+  [[maybe_unused]] uint4* i8_bufs = reinterpret_cast<uint4*>(xw_all + 8 * 128);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -703,7 +742,8 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
         epilogue_f32_staged<BN>(ti.second ? args2 : args, ti.g, ti.row0 + quarter * 32, ti.row_end, t_row, lane,
                                 xw_all + quarter * 32 * 32);
       else if constexpr (is_i8(EPI))
-        epilogue_i8<EPI, BN>(ti.second ? args2 : args, ti, row, sa, i8_sc, t_row, (warp - 2) >> 2);
+        epilogue_i8<EPI, BN>(ti.second ? args2 : args, ti, row - lane, sa, i8_sc, t_row, (warp - 2) >> 2,
+                             i8_bufs + (warp - 2) * 128, lane);
       else
         epilogue_rows<EPI, BN>(ti.second ? args2 : args, ti.g, row, row < ti.row_end, ti.n0, t_row);
       tc_fence_before_sync();
@@ -953,6 +993,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
   int* prefix2 = prefix + kMaxGroups + 1;
   float* xbuf = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(prefix2 + kMaxGroups + 1) + 15) & ~uintptr_t(15));
   [[maybe_unused]] float* i8_scales = xbuf + 32 * kSwapXStride;
+  // 8-bit epilogues of full tiles: 2 KB per warp of the swap tiles' buffer (all
+  // epilogue warps pass a barrier between two tiles)
+  [[maybe_unused]] uint4* i8_bufs = reinterpret_cast<uint4*>(xbuf);
+  static_assert(8 * 2048 <= kSwapXBytes, "staging of the 8-bit epilogues");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -1215,7 +1259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
       } else {
         const int row = ti.row0 + 128 * static_cast<int>(rank) + r;
         if constexpr (is_i8(EPI))
-          epilogue_i8<EPI, kPairBN>(A, ti, row, sa, i8_sc, t_row, half);
+          epilogue_i8<EPI, kPairBN>(A, ti, row - lane, sa, i8_sc, t_row, half, i8_bufs + (warp - 2) * 128, lane);
         else
           epilogue_rows<EPI, kPairBN>(A, ti.g, row, row < ti.row_end, ti.n0, t_row);
       }
