@@ -1246,7 +1246,9 @@ static cudaError_t run_few(const FewArgs& a, int64_t ctas, cudaStream_t st) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_layer_kernel<WT>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, few_layer_kernel<WT>, a);
+  if (e != cudaSuccess) cudaGetLastError();  // reported to the caller, not left for the next CUDA call
+  return e;
 }
 
 cudaError_t launch_few_layer(const Problem& p, const FewCall& c, cudaStream_t st) {

@@ -78,10 +78,36 @@ class MoeLayer:
         if y is None:
             y = torch.empty((self.prob.T, self.prob.d_model), dtype=self.dtype, device=self.device)
         if self.few_ws is None:
+            self._check_weights()
             self.few_ws = api.alloc_few_workspace(self.prob, self.device)
         self._forward_few(self.prob, x, self.weights, y, self.routing, self.stats if with_stats else None,
                           self.few_ws, stream)
         return y
+
+    def _weight_shapes(self) -> dict:
+        """Expected (shape, dtype) of the weights a forward reads."""
+        P = self.prob
+        E, d, F, Ns = P.n_experts, P.d_model, P.d_ff, P.n_shared
+        out = {"w13": ((E, 2 * F, d), self.dtype), "w2": ((E, d, F), self.dtype)}
+        if not P.flags & api.FLAG_LOGITS_GIVEN:
+            out["w_gate"] = ((E, d), self.dtype)
+        if Ns:
+            out.update(w13_shared=((Ns, 2 * F, d), self.dtype), w2_shared=((Ns, d, F), self.dtype))
+        return out
+
+    def _check_weights(self) -> None:
+        """Raise ValueError unless the weights have the problem's shapes and types."""
+        E = self.prob.n_experts
+        for name, (shape, dtype) in self._weight_shapes().items():
+            t = self.weights.get(name)
+            if t is None or tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"weights['{name}'] must be a contiguous CUDA {dtype} tensor of shape {shape}")
+        for name, dtype in (("logit_offset", torch.float32), ("sel_bias", torch.float32),
+                            ("expert_capacity", torch.int32)):
+            t = self.weights.get(name)
+            if t is not None and (tuple(t.shape) != (E,) or t.dtype != dtype or not t.is_cuda or
+                                  not t.is_contiguous()):
+                raise ValueError(f"weights['{name}'] must be a contiguous CUDA {dtype} tensor of shape {(E,)}")
 
     def capture(self, with_stats: bool = True) -> None:
         """Capture one forward into a CUDA graph over static input/output
@@ -232,6 +258,23 @@ class MoeLayerI8(MoeLayer):
     _alloc_workspace = staticmethod(api.alloc_i8_workspace)
     _forward = staticmethod(api.moe_layer_forward_i8)
     _forward_few = staticmethod(api.moe_layer_forward_few_i8)
+
+    def __init__(self, prob: api.MoeProblem, weights: dict, device="cuda", keep_routing: bool = True):
+        super().__init__(prob, weights, device, keep_routing)
+        self._check_weights()
+
+    def _weight_shapes(self) -> dict:
+        P = self.prob
+        E, d, F, Ns = P.n_experts, P.d_model, P.d_ff, P.n_shared
+        i8, f32 = torch.int8, torch.float32
+        out = {"w13": ((E, 2 * F, d), i8), "w13_scale": ((E, 2 * F), f32), "w2": ((E, d, F), i8),
+               "w2_scale": ((E, d), f32)}
+        if not P.flags & api.FLAG_LOGITS_GIVEN:
+            out["w_gate"] = ((E, d), self.dtype)
+        if Ns:
+            out.update(w13_shared=((Ns, 2 * F, d), i8), w13_shared_scale=((Ns, 2 * F), f32),
+                       w2_shared=((Ns, d, F), i8), w2_shared_scale=((d,), f32))
+        return out
 
     @classmethod
     def from_layer(cls, layer: MoeLayer, keep_routing: bool = True) -> "MoeLayerI8":

@@ -104,7 +104,9 @@ def expert(x, w13, w2, bf16: bool):
 
 def few_layer(inp: dict, K: int, caps, bf16: bool, bias_on_logit=False, logits=None):
     """The layer from CPU inputs: dict of routing, y and its bound (before the
-    rounding to the activations' type)."""
+    rounding to the activations' type), and mag, the magnitudes of the expert
+    outputs that make up y (times their gates): a form that rounds them to BF16
+    first is off by 2^-8 mag more."""
     x = inp["x"].double()
     T, d = x.shape
     E = inp["w13"].shape[0]
@@ -118,7 +120,7 @@ def few_layer(inp: dict, K: int, caps, bf16: bool, bias_on_logit=False, logits=N
     idx, w, p = route(logits, K, None if bias is None else torch.as_tensor(bias), bias_on_logit)
     counts, kept, off, slot = dispatch(idx, E, caps)
     y = torch.zeros((T, d), dtype=torch.float64)
-    ey = torch.zeros_like(y)
+    ey, mag = torch.zeros_like(y), torch.zeros_like(y)
     if i8:
         q, s = quantize(inp["x"])
     if inp.get("w13_shared") is not None:
@@ -128,11 +130,11 @@ def few_layer(inp: dict, K: int, caps, bf16: bool, bias_on_logit=False, logits=N
             w13 = torch.cat([inp["w13_shared"][:, :F].reshape(Ns * F, d), inp["w13_shared"][:, F:].reshape(Ns * F, d)])
             s13 = torch.cat([inp["w13_shared_scale"][:, :F].reshape(-1), inp["w13_shared_scale"][:, F:].reshape(-1)])
             a, b = ffn_i8(q, s, w13, s13, inp["w2_shared"].permute(1, 0, 2).reshape(d, Ns * F), inp["w2_shared_scale"])
-            y, ey = y + a, ey + b
+            y, ey, mag = y + a, ey + b, mag + a.abs()
         else:
             for n in range(Ns):
                 a, b = expert(x, inp["w13_shared"][n], inp["w2_shared"][n], bf16)
-                y, ey = y + a, ey + b
+                y, ey, mag = y + a, ey + b, mag + a.abs()
     for e in range(E):
         tok, k = torch.nonzero((idx == e) & (slot >= 0), as_tuple=True)
         if len(tok) == 0:
@@ -143,6 +145,7 @@ def few_layer(inp: dict, K: int, caps, bf16: bool, bias_on_logit=False, logits=N
             a, b = expert(x[tok], inp["w13"][e], inp["w2"][e], bf16)
         y[tok] += w[tok, k][:, None] * a
         ey[tok] += w[tok, k][:, None] * (b + 8 * U * a.abs())
+        mag[tok] += w[tok, k][:, None] * a.abs()
     ey = ey + (K + 8) * U * y.abs()
     return dict(logits=logits, topk_idx=idx.int(), topk_w=w, p=p, counts=counts, kept=kept, seg_off=off, slot_of=slot,
-                y=y, bound=ey)
+                y=y, bound=ey, mag=mag)
