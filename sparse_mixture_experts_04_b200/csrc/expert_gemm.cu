@@ -2101,30 +2101,37 @@ static bool i8_single_problem(const I8Gemm& g, bool swiglu, int bn, SingleProble
   return true;
 }
 
-// Tile shape by the rows a group is expected to hold, as the BF16 products.
-static bool i8_pairs(const I8Gemm& g) {
+// Tile shape by the rows a group is expected to hold, as the BF16 products
+// (measured again with 8-bit operands: 64 experts, d = 2048, F = 1408, single
+// CTAs 125 / 137 / 183 us against 162 / 199 / 201 us on pairs at 64 / 128 / 255
+// rows per expert).  Single CTAs: 256 B rows per tile, or 64 where 256 would
+// leave SMs without a tile (one row, K = 2048, N = 2816: 11 tiles 9.9 us, 44 tiles
+// 8.8 us).
+enum { kI8Narrow = 0, kI8Single = 1, kI8Pair = 2 };
+
+static int i8_shape(const I8Gemm& g, bool swiglu) {
   const int64_t expected = g.seg_off ? g.n_rows / g.n_groups : g.n_rows;
-  return tile_mode(expected) != kTileSingle;
+  if (tile_mode(expected) != kTileSingle) return kI8Pair;
+  const int64_t blocks = cdiv(g.n_rows, kBM) + (g.n_groups < g.n_rows ? g.n_groups : g.n_rows) - 1;
+  return blocks * cdiv(g.N, swiglu ? 128 : 256) < num_sms() ? kI8Narrow : kI8Single;
 }
 
+// One product, or two of the same shape in one launch (their tiles interleaved).
 template <int EPI>
-static int run_i8(const I8Gemm& g, cudaStream_t st) {
-  if (g.n_rows <= 0) return 0;
-  if (i8_pairs(g)) {
-    PairProblem q;
-    if (!i8_pair_problem(g, EPI == EPI_I8_SWIGLU, &q)) return -3;
-    return run_pair_gemm<EPI>(q, nullptr, st);
-  }
-  // 256 B rows per tile, or 64 where 256 would leave SMs without a tile (one row,
-  // K = 2048, N = 2816: 11 tiles 9.9 us, 44 tiles 8.8 us)
+static int run_i8(const I8Gemm& g, cudaStream_t st, const I8Gemm* g2 = nullptr) {
   constexpr bool kSwiglu = EPI == EPI_I8_SWIGLU;
-  const int64_t blocks = cdiv(g.n_rows, kBM) + (g.n_groups < g.n_rows ? g.n_groups : g.n_rows) - 1;
-  SingleProblem q;
-  if (blocks * cdiv(g.N, kSwiglu ? 128 : 256) < num_sms()) {
-    if (!i8_single_problem(g, kSwiglu, 64, &q)) return -3;
-    return run_gemm<EPI, 64, 8>(q.ta, q.tb, q.a, q.tile_bound, st);
+  if (g.n_rows <= 0) return 0;
+  const int shape = i8_shape(g, kSwiglu);
+  if (shape == kI8Pair) {
+    PairProblem q, q2;
+    if (!i8_pair_problem(g, kSwiglu, &q) || (g2 && !i8_pair_problem(*g2, kSwiglu, &q2))) return -3;
+    return run_pair_gemm<EPI>(q, g2 ? &q2 : nullptr, st);
   }
-  if (!i8_single_problem(g, kSwiglu, 256, &q)) return -3;
+  const int bn = shape == kI8Narrow && !g2 ? 64 : 256;
+  SingleProblem q, q2;
+  if (!i8_single_problem(g, kSwiglu, bn, &q) || (g2 && !i8_single_problem(*g2, kSwiglu, bn, &q2))) return -3;
+  if (bn == 64) return run_gemm<EPI, 64, 8>(q.ta, q.tb, q.a, q.tile_bound, st);
+  if (g2) return run_gemm<EPI, 256, 4>(q.ta, q.tb, q.a, q.tile_bound, st, &q2.ta, &q2.tb, &q2.a, q2.tile_bound);
   return run_gemm<EPI, 256, 4>(q.ta, q.tb, q.a, q.tile_bound, st);
 }
 
@@ -2155,51 +2162,72 @@ int launch_matmul_i8(const int8_t* x, const float* x_scale, int64_t n_rows, cons
 // are one row of N_s F integers with one scale per token, and w2_scale [d] is
 // the scale of an output channel over all of them, so the down product sums
 // the N_s experts in the integer accumulator.
-int launch_expert_ffn_i8(const Problem& p, int mode, const int8_t* x, const float* x_scale, int64_t n_rows,
-                         const int32_t* seg_off, const int8_t* w13, const float* w13_scale, const int8_t* w2,
-                         const float* w2_scale, float* h, unsigned* amax, int8_t* hq, float* h_scale, void* y,
-                         unsigned* status, cudaStream_t st, bool amax_cleared) {
-  if (n_rows <= 0) return 0;
+static I8Gemm i8_up(const Problem& p, bool routed, const FfnI8& f, unsigned* status) {
+  I8Gemm g{};
+  g.a = f.x;
+  g.a_scale = f.x_scale;
+  g.n_rows = f.n_rows;
+  g.seg_off = routed ? f.seg_off : nullptr;
+  g.n_groups = routed ? p.E : p.Ns;
+  g.w = f.w13;
+  g.w_scale = f.w13_scale;
+  g.w_scale_stride = 2 * static_cast<int64_t>(p.F);
+  g.N = p.F;
+  g.K = p.d;
+  g.k_groups = 1;
+  g.out = f.h;
+  g.ldo = routed ? p.F : static_cast<int64_t>(p.Ns) * p.F;
+  g.out_col_stride = routed ? 0 : p.F;
+  g.row_amax = f.amax;
+  g.status = status;
+  return g;
+}
+
+static I8Gemm i8_down(const Problem& p, bool routed, const FfnI8& f, unsigned* status) {
+  I8Gemm g{};
+  g.a = f.hq;
+  g.a_scale = f.h_scale;
+  g.n_rows = f.n_rows;
+  g.seg_off = routed ? f.seg_off : nullptr;
+  g.n_groups = routed ? p.E : 1;
+  g.w = f.w2;
+  g.w_scale = f.w2_scale;
+  g.w_scale_stride = p.d;
+  g.N = p.d;
+  g.K = p.F;
+  g.k_groups = routed ? 1 : p.Ns;
+  g.out = f.y;
+  g.ldo = p.d;
+  g.status = status;
+  return g;
+}
+
+int launch_expert_ffn_i8(const Problem& p, int mode, const FfnI8& f, unsigned* status, cudaStream_t st,
+                         bool amax_cleared) {
+  if (f.n_rows <= 0) return 0;
   const bool routed = mode == 0;
-  const int h_cols = routed ? p.F : p.Ns * p.F;
-  if (!amax_cleared && cudaMemsetAsync(amax, 0, static_cast<size_t>(n_rows) * sizeof(unsigned), st) != cudaSuccess) return -3;
-  I8Gemm up{};
-  up.a = x;
-  up.a_scale = x_scale;
-  up.n_rows = n_rows;
-  up.seg_off = routed ? seg_off : nullptr;
-  up.n_groups = routed ? p.E : p.Ns;
-  up.w = w13;
-  up.w_scale = w13_scale;
-  up.w_scale_stride = 2 * static_cast<int64_t>(p.F);
-  up.N = p.F;
-  up.K = p.d;
-  up.k_groups = 1;
-  up.out = h;
-  up.ldo = h_cols;
-  up.out_col_stride = routed ? 0 : p.F;
-  up.row_amax = amax;
-  up.status = status;
-  if (int rc = run_i8<EPI_I8_SWIGLU>(up, st)) return rc;
-  if (launch_quantize_hidden(h, amax, routed ? seg_off + p.E : nullptr, n_rows, h_cols, hq, h_scale, st) !=
-      cudaSuccess)
+  if (!amax_cleared && launch_clear_amax(f.amax, f.n_rows, st) != cudaSuccess) return -3;
+  if (int rc = run_i8<EPI_I8_SWIGLU>(i8_up(p, routed, f, status), st)) return rc;
+  if (launch_quantize_hidden(f.h, f.amax, routed ? f.seg_off + p.E : nullptr, f.n_rows, routed ? p.F : p.Ns * p.F, f.hq,
+                             f.h_scale, st) != cudaSuccess)
     return -3;
-  I8Gemm dn{};
-  dn.a = hq;
-  dn.a_scale = h_scale;
-  dn.n_rows = n_rows;
-  dn.seg_off = up.seg_off;
-  dn.n_groups = routed ? p.E : 1;
-  dn.w = w2;
-  dn.w_scale = w2_scale;
-  dn.w_scale_stride = p.d;
-  dn.N = p.d;
-  dn.K = p.F;
-  dn.k_groups = routed ? 1 : p.Ns;
-  dn.out = y;
-  dn.ldo = p.d;
-  dn.status = status;
-  return run_i8<EPI_I8_OUT>(dn, st);
+  return run_i8<EPI_I8_OUT>(i8_down(p, routed, f, status), st);
+}
+
+int launch_layer_ffn_i8(const Problem& p, const FfnI8& r, const FfnI8& s, unsigned* status, cudaStream_t st) {
+  const I8Gemm ur = i8_up(p, true, r, status), us = i8_up(p, false, s, status);
+  const I8Gemm dr = i8_down(p, true, r, status), ds = i8_down(p, false, s, status);
+  const bool mixed = r.n_rows > 0 && (i8_shape(ur, true) == kI8Pair) == (i8_shape(us, true) == kI8Pair) &&
+                     (i8_shape(dr, false) == kI8Pair) == (i8_shape(ds, false) == kI8Pair);
+  if (!mixed) {
+    if (int rc = launch_expert_ffn_i8(p, 0, r, status, st, true)) return rc;
+    return launch_expert_ffn_i8(p, 1, s, status, st, true);
+  }
+  if (int rc = run_i8<EPI_I8_SWIGLU>(ur, st, &us)) return rc;
+  if (launch_quantize_hidden(r.h, r.amax, r.seg_off + p.E, r.n_rows, p.F, r.hq, r.h_scale, st, s.h, s.amax, s.n_rows,
+                             p.Ns * p.F, s.hq, s.h_scale) != cudaSuccess)
+    return -3;
+  return run_i8<EPI_I8_OUT>(dr, st, &ds);
 }
 
 }  // namespace moe

@@ -201,16 +201,38 @@ cudaError_t launch_quantize_dispatch(const Problem& p, const void* x, const int3
 // count of the rows to quantise, at most n_rows.
 cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t n_rows, int n_cols, int8_t* q, float* scale,
                                  cudaStream_t st);
+// h2 (or nullptr): a second set of rows in the same launch, all of them.
 cudaError_t launch_quantize_hidden(const float* h, const unsigned* amax, const int32_t* n_live, int64_t n_rows,
-                                   int n_cols, int8_t* q, float* scale, cudaStream_t st);
+                                   int n_cols, int8_t* q, float* scale, cudaStream_t st, const float* h2 = nullptr,
+                                   const unsigned* amax2 = nullptr, int64_t n_rows2 = 0, int n_cols2 = 0,
+                                   int8_t* q2 = nullptr, float* scale2 = nullptr);
+cudaError_t launch_clear_amax(unsigned* amax, int64_t n, cudaStream_t st);
 // expert_gemm.cu: 8-bit products (moe_matmul_i8, moe_expert_ffn_i8); return a moe_status value
 int launch_matmul_i8(const int8_t* x, const float* x_scale, int64_t n_rows, const int32_t* seg_off, int n_groups,
                      const int8_t* w, const float* w_scale, int N, int K, int out_dtype, void* y, unsigned* status,
                      cudaStream_t st);
-int launch_expert_ffn_i8(const Problem& p, int mode, const int8_t* x, const float* x_scale, int64_t n_rows,
-                         const int32_t* seg_off, const int8_t* w13, const float* w13_scale, const int8_t* w2,
-                         const float* w2_scale, float* h, unsigned* amax, int8_t* hq, float* h_scale, void* y,
-                         unsigned* status, cudaStream_t st, bool amax_cleared = false);
+// One expert FFN on 8-bit rows: its operands and scratch.
+struct FfnI8 {
+  const int8_t* x;
+  const float* x_scale;
+  int64_t n_rows;
+  const int32_t* seg_off;  // routed; shared: nullptr
+  const int8_t* w13;
+  const float* w13_scale;
+  const int8_t* w2;
+  const float* w2_scale;
+  float* h;          // [n_rows, F] (shared: N_s F)
+  unsigned* amax;    // [n_rows]
+  int8_t* hq;
+  float* h_scale;
+  void* y;
+};
+// mode 0 routed, 1 shared; clears amax first unless it is clear already.
+int launch_expert_ffn_i8(const Problem& p, int mode, const FfnI8& f, unsigned* status, cudaStream_t st,
+                         bool amax_cleared = false);
+// Routed and shared experts (amax of both clear), in the same launches when
+// both take the same tile shape.
+int launch_layer_ffn_i8(const Problem& p, const FfnI8& routed, const FfnI8& shared, unsigned* status, cudaStream_t st);
 
 // grad_gemm.cu: backward of the expert FFNs (see there); returns a moe_status value
 // gu_ready: gu already holds the forward's gate/up projections (no recompute)

@@ -759,10 +759,10 @@ int moe_expert_ffn_i8(const moe_problem_t* q, int32_t mode, const int8_t* x_rows
   if (mode == MOE_FFN_SHARED && (p.Ns < 1 || n_rows > p.T)) return MOE_ERR_INVALID_ARG;
   const I8Layout L = make_i8_layout(p);
   const bool routed = mode == MOE_FFN_ROUTED;
-  return launch_expert_ffn_i8(p, mode, x_rows, x_scale, n_rows, seg_off, w13, w13_scale, w2, w2_scale,
-                              at<float>(ws, routed ? L.h : L.hs), at<unsigned>(ws, routed ? L.amax : L.amax_s),
-                              at<int8_t>(ws, routed ? L.hq : L.hsq), at<float>(ws, routed ? L.h_scale : L.hs_scale),
-                              y_rows, at<unsigned>(ws, L.base.status), reinterpret_cast<cudaStream_t>(stream))
+  const FfnI8 f{x_rows, x_scale, n_rows, seg_off, w13, w13_scale, w2, w2_scale, at<float>(ws, routed ? L.h : L.hs),
+                at<unsigned>(ws, routed ? L.amax : L.amax_s), at<int8_t>(ws, routed ? L.hq : L.hsq),
+                at<float>(ws, routed ? L.h_scale : L.hs_scale), y_rows};
+  return launch_expert_ffn_i8(p, mode, f, at<unsigned>(ws, L.base.status), reinterpret_cast<cudaStream_t>(stream))
              ? MOE_ERR_CUDA
              : MOE_OK;
 }
@@ -807,16 +807,13 @@ int moe_layer_forward_i8(const moe_problem_t* q, const void* x, const moe_weight
                                                at<unsigned>(ws, L.amax), shared ? at<int8_t>(ws, L.xs_q) : nullptr,
                                                at<float>(ws, L.xs_scale), at<unsigned>(ws, L.amax_s), st))
     return cuda_rc(e);
-  if (p.max_rows > 0 &&
-      launch_expert_ffn_i8(p, MOE_FFN_ROUTED, at<int8_t>(ws, L.x_q), at<float>(ws, L.x_scale), p.max_rows, seg_off,
-                           w->w13, w->w13_scale, w->w2, w->w2_scale, at<float>(ws, L.h), at<unsigned>(ws, L.amax),
-                           at<int8_t>(ws, L.hq), at<float>(ws, L.h_scale), at<void>(ws, B.y_perm), status, st, true))
-    return MOE_ERR_CUDA;
-  if (shared &&
-      launch_expert_ffn_i8(p, MOE_FFN_SHARED, at<int8_t>(ws, L.xs_q), at<float>(ws, L.xs_scale), p.T, nullptr,
-                           w->w13_shared, w->w13_shared_scale, w->w2_shared, w->w2_shared_scale, at<float>(ws, L.hs),
-                           at<unsigned>(ws, L.amax_s), at<int8_t>(ws, L.hsq), at<float>(ws, L.hs_scale),
-                           at<void>(ws, B.y_shared), status, st, true))
+  const FfnI8 fr{at<int8_t>(ws, L.x_q), at<float>(ws, L.x_scale), p.max_rows, seg_off, w->w13, w->w13_scale, w->w2,
+                 w->w2_scale, at<float>(ws, L.h), at<unsigned>(ws, L.amax), at<int8_t>(ws, L.hq),
+                 at<float>(ws, L.h_scale), at<void>(ws, B.y_perm)};
+  const FfnI8 fs{at<int8_t>(ws, L.xs_q), at<float>(ws, L.xs_scale), p.T, nullptr, w->w13_shared, w->w13_shared_scale,
+                 w->w2_shared, w->w2_shared_scale, at<float>(ws, L.hs), at<unsigned>(ws, L.amax_s),
+                 at<int8_t>(ws, L.hsq), at<float>(ws, L.hs_scale), at<void>(ws, B.y_shared)};
+  if (shared ? launch_layer_ffn_i8(p, fr, fs, status, st) : launch_expert_ffn_i8(p, MOE_FFN_ROUTED, fr, status, st, true))
     return MOE_ERR_CUDA;
   return cuda_rc(launch_combine(p, at<void>(ws, B.y_perm), slot_of, gw, shared ? at<void>(ws, B.y_shared) : nullptr, y,
                                 st));

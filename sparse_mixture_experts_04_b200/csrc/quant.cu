@@ -6,6 +6,8 @@
 //
 // Both are bound by memory: one read of the row, one write of a byte per
 // element.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"
@@ -261,50 +263,77 @@ cudaError_t launch_quantize_dispatch(const Problem& p, const void* x, const int3
                   xs_scale, amax_s);
 }
 
-// h [*, n_cols] FP32, amax [*] bits of each row's largest magnitude; rows
-// [0, min(*n_live, n_rows)) (n_live NULL: n_rows).  A warp takes 512 columns of
-// a row at a time: four coalesced 16-byte loads per lane in flight.
-__global__ void __launch_bounds__(kQuantThreads) quantize_hidden_kernel(const float* __restrict__ h,
-                                                                        const unsigned* __restrict__ amax,
-                                                                        const int32_t* __restrict__ n_live,
-                                                                        int n_rows, int n_cols,
-                                                                        int8_t* __restrict__ q,
-                                                                        float* __restrict__ scale) {
+// A kernel, not a memset, so that the product behind it may start early
+// (programmatic dependent launch).
+__global__ void __launch_bounds__(kQuantThreads) clear_amax_kernel(unsigned* __restrict__ amax, int64_t n) {
   pdl_wait();
   pdl_trigger();
-  const int rows = n_live ? min(max(*n_live, 0), n_rows) : n_rows;
-  const int pieces = (n_cols + 511) / 512, lane = threadIdx.x & 31;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    amax[i] = 0;
+}
+
+cudaError_t launch_clear_amax(unsigned* amax, int64_t n, cudaStream_t st) {
+  int64_t grid = (n + kQuantThreads - 1) / kQuantThreads;
+  if (grid > 1024) grid = 1024;
+  return launch_k(clear_amax_kernel, dim3(static_cast<unsigned>(grid)), dim3(kQuantThreads), 0, st, amax, n);
+}
+
+// FP32 rows h [*, n_cols], amax [*] bits of each row's largest magnitude; rows
+// [0, min(*n_live, n_rows)) (n_live NULL: n_rows).  A warp takes 512 columns of
+// a row at a time: four coalesced 16-byte loads per lane in flight.
+// blockIdx.y selects one of two sets of rows (routed, shared).
+struct HiddenRows {
+  const float* h;
+  const unsigned* amax;
+  const int32_t* n_live;
+  int n_rows, n_cols;
+  int8_t* q;
+  float* scale;
+};
+
+__global__ void __launch_bounds__(kQuantThreads) quantize_hidden_kernel(const HiddenRows a0, const HiddenRows a1) {
+  pdl_wait();
+  pdl_trigger();
+  const HiddenRows a = blockIdx.y ? a1 : a0;
+  const int rows = a.n_live ? min(max(*a.n_live, 0), a.n_rows) : a.n_rows;
+  const int pieces = (a.n_cols + 511) / 512, lane = threadIdx.x & 31;
   const int64_t total = static_cast<int64_t>(rows) * pieces;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5); i < total; i += warps) {
     const int row = static_cast<int>(i / pieces);
     const int c0 = static_cast<int>(i - static_cast<int64_t>(row) * pieces) * 512 + lane * 4;
-    const float* hr = h + static_cast<int64_t>(row) * n_cols;
+    const float* hr = a.h + static_cast<int64_t>(row) * a.n_cols;
     float4 v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (c0 + j * 128 < n_cols) v[j] = __ldcs(reinterpret_cast<const float4*>(hr + c0 + j * 128));
-    const float s = quant_scale(amax[row]);
+      if (c0 + j * 128 < a.n_cols) v[j] = __ldcs(reinterpret_cast<const float4*>(hr + c0 + j * 128));
+    const float s = quant_scale(a.amax[row]);
     const float inv = 1.0f / s;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (c0 + j * 128 < n_cols) {
+      if (c0 + j * 128 < a.n_cols) {
         const float f[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-        *reinterpret_cast<uint32_t*>(q + static_cast<int64_t>(row) * n_cols + c0 + j * 128) = quant_pack4(f, s, inv);
+        *reinterpret_cast<uint32_t*>(a.q + static_cast<int64_t>(row) * a.n_cols + c0 + j * 128) =
+            quant_pack4(f, s, inv);
       }
     }
-    if (c0 == 0) scale[row] = s;
+    if (c0 == 0) a.scale[row] = s;
   }
 }
 
 cudaError_t launch_quantize_hidden(const float* h, const unsigned* amax, const int32_t* n_live, int64_t n_rows,
-                                   int n_cols, int8_t* q, float* scale, cudaStream_t st) {
-  const int64_t pieces = n_rows * ((n_cols + 511) / 512);
+                                   int n_cols, int8_t* q, float* scale, cudaStream_t st, const float* h2,
+                                   const unsigned* amax2, int64_t n_rows2, int n_cols2, int8_t* q2, float* scale2) {
+  const HiddenRows a{h, amax, n_live, static_cast<int>(n_rows), n_cols, q, scale};
+  const HiddenRows b{h2, amax2, nullptr, static_cast<int>(n_rows2), n_cols2, q2, scale2};
+  int64_t pieces = n_rows * ((n_cols + 511) / 512);
+  if (h2) pieces = std::max(pieces, n_rows2 * ((n_cols2 + 511) / 512));
   int64_t grid = (pieces + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
   const int64_t most = static_cast<int64_t>(num_sms()) * 8;
   if (grid > most) grid = most;
-  return launch_k(quantize_hidden_kernel, dim3(static_cast<unsigned>(grid)), dim3(kQuantThreads), 0, st, h, amax,
-                  n_live, static_cast<int>(n_rows), n_cols, q, scale);
+  return launch_k(quantize_hidden_kernel, dim3(static_cast<unsigned>(grid), h2 ? 2 : 1), dim3(kQuantThreads), 0, st, a,
+                  b);
 }
 
 }  // namespace moe
