@@ -24,18 +24,29 @@
 // depend on no other CTA), so a barrier costs no bandwidth.
 //
 // Arithmetic: BF16 and 8-bit weights are the M operand of m16n8k16 / m16n8k32
-// tensor-core instructions (16 weight rows, 8 tokens), the 8 warps taking
-// 64-byte slices of the reduction in turn; the products of a unit are 16 x 8
-// numbers per warp, summed over the warps in shared memory in warp order.  The
+// tensor-core instructions (16 weight rows, 8 tokens).  Two teams of 4 warps
+// take a unit each; the warps of a team take 64-byte slices of the reduction in
+// turn, and their 16 x 8 sums are added in shared memory in warp order.  The
 // tensor cores are nearly idle (a stage of 32 KB arrives in 1400 cycles and is
-// multiplied in some 250), which is why the simple warp-level instruction is
+// multiplied in some 500), which is why the simple warp-level instruction is
 // used and not tcgen05: its 128-row tiles would be 1..8 rows full.  FP32
-// weights take fused multiply-adds (8 rows x 8 tokens per lane).  No step
-// depends on the order in which CTAs run, so results repeat bit for bit.
+// weights take fused multiply-adds (8 rows x 8 tokens per lane).  Sums are FP32
+// or int32; BF16 layers round the hidden rows to BF16, as moe_layer_forward
+// does (they are the tensor cores' operand), and nothing else before y.  No
+// step depends on the order in which CTAs run, so results repeat bit for bit.
 //
-// Every wait on the ring is bounded (mbar_wait); after a time-out the kernel
+// What bounds it: the weights' stream.  us per call, and of the measured copy
+// bandwidth (6540 GB/s) that the weights alone make up: 32 tokens, d = 4096,
+// E = 128, F = 1536, top-8 + 1 shared 640 (1.0); one token, d = 4096, E = 8,
+// F = 14336, top-2 127 (0.85); one token, d = 2048, E = 128, F = 1024, top-8 + 4
+// shared 51 (0.45).  The last is where the rest shows: 12 us until the experts are
+// known (logits 3, barrier 2, top-K 5, slots 2), three more grid barriers of 1.7
+// us, 3 us for the combine, 4 us between two launches.
+//
+// Every wait is bounded (mbar_wait, few_grid_sync); after a time-out the kernel
 // issues no more copies, waits for those in flight and reports
-// MOE_DEV_WAIT_TIMEOUT.  The grid barriers are cooperative groups' own: all
+// MOE_DEV_WAIT_TIMEOUT.  The first grid barrier is cooperative groups' own,
+// which needs no cleared memory, and clears the counters of the others.  All
 // CTAs are resident (cooperative launch) and each reaches every barrier.
 #include <cooperative_groups.h>
 #include <math.h>
@@ -50,7 +61,6 @@
 namespace moe {
 
 namespace cg = cooperative_groups;
-
 
 // Variants: the weights' type; kFewBF16Many trades half of the ring for a token
 // buffer of twice the rows (see few_tiling).
@@ -314,12 +324,15 @@ struct Few : FewTile<WT> {
   }
 };
 
-// The copy side (a warp for each half of a stage's rows, every lane alike).
-// Each team has its own ring of
-// kFewStages / teams stages, so that a team never waits for a phase of a barrier
-// more than one ahead (a parity wait could not tell it from the past one).  The
-// teams' units of a span are copied together, a stage of each in turn: stage k
-// of units i, i + 1, then stage k + 1 of both.
+// The copy side (kCopiers warps, each its own rows of every stage; every lane
+// of a warp holds the same Cursor).  Warps of their own: issuing the 16 copies
+// of a stage takes some 800 cycles, which the products waited for while the same
+// warps did both (32 tokens, d = 4096, E = 128: 1583 -> 781 us with one copying
+// warp, 774 -> 648 us with two).  Each team has its own ring of kFewStages /
+// teams stages, so that a team never waits for a phase of a barrier more than
+// one ahead (a parity wait could not tell it from the past one).  The teams'
+// units of a span are copied together, a stage of each in turn: stage k of
+// units i, i + 1, then stage k + 1 of both.
 struct Cursor {
   int pass = 0, u = 0, end = 0;  // next unit of the pass, the pass's last
   int left = 0, off = 0;         // units left in the span, bytes of the current units' rows copied
