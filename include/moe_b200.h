@@ -416,7 +416,7 @@ int moe_layer_forward_few(const moe_problem_t* p, const void* x, const moe_weigh
  * 8-bit integers.
  *
  * A row v is held as int8 q and one FP32 scale s:
- *   s = max(fl32(max|v| / 127), 2^-126),  q = the integer nearest to v / s
+ *   s = max(fl32(max|v| * fl32(1 / 127)), 2^-126),  q = the integer nearest to v / s
  * (of the real quotient, ties to even), -127 <= q <= 127, v ~ q s.  A row with
  * an infinity or a NaN gets s = NaN, q = 0: whatever is computed from it is
  * NaN, other rows are not touched.

@@ -1,8 +1,12 @@
 // Symmetric 8-bit quantisation of a row, shared by the kernels that quantise
 // token rows, hidden rows and (at load time) weights.
 //
-//   scale = max(fl32(max|v| / 127), 2^-126)
+//   scale = max(fl32(max|v| * fl32(1 / 127)), 2^-126)
 //   q     = the integer nearest to v / scale, ties to even, in [-127, 127]
+//
+// (The product with the rounded 1 / 127, not the quotient: it is what torch
+// computes on the GPU for a division by a constant, so rows quantised with
+// elementary torch operations have the same scales, bit for bit.)
 //
 // The floor keeps the scale normal (and 1 / scale finite) for rows of zeros
 // and of subnormal numbers.  A row holding an infinity or a NaN gets the scale
@@ -26,7 +30,7 @@ constexpr float kQuantScaleFloor = 1.17549435e-38f;  // 2^-126
 // amax as raw bits of a non-negative float (NaN above infinity above the rest)
 __device__ __forceinline__ float quant_scale(unsigned amax_bits) {
   if (amax_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-  return fmaxf(__fdiv_rn(__uint_as_float(amax_bits), 127.0f), kQuantScaleFloor);
+  return fmaxf(__uint_as_float(amax_bits) * (1.0f / 127.0f), kQuantScaleFloor);
 }
 
 __device__ __forceinline__ unsigned abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }

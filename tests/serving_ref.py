@@ -20,11 +20,12 @@ SILU = 2.0 ** -18
 
 
 def quantize(x: torch.Tensor):
-    """(q float64 integers, scale float64) of rows: s = max(fl32(max|v| / 127),
-    2^-126), q the nearest integer to v / s, ties to even; non-finite rows NaN, 0."""
+    """(q float64 integers, scale float64) of rows: s = max(fl32(max|v| *
+    fl32(1 / 127)), 2^-126), q the nearest integer to v / s, ties to even;
+    non-finite rows NaN, 0."""
     x = x.double()
-    amax = x.abs().amax(-1)
-    s = (amax / 127.0).float().clamp(min=2.0 ** -126).double()
+    amax = x.abs().amax(-1).float()
+    s = (amax * torch.tensor(1.0 / 127.0, dtype=torch.float32)).clamp(min=2.0 ** -126).double()
     q = torch.round(x / s[..., None])
     bad = ~torch.isfinite(x).all(-1)
     s[bad] = math.nan
