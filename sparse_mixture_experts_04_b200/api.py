@@ -279,11 +279,17 @@ def _cuda(name: str, t: torch.Tensor) -> int:
     return t.get_device()
 
 
+# The handle of a device's current stream.  torch's own shortcut to it where it
+# has one (0.1 us; building a Stream object takes 1.3 us of a 10 us call).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _enqueue(name: str, dev: int, stream, *args) -> None:
     """Call the C entry point `name` with args and the stream handle (`stream`,
     or device dev's current stream), device dev being current."""
     fn = getattr(_lib.lib(), name)
-    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    st = _current_stream(dev) if stream is None else _stream(stream)
     if torch.cuda.current_device() == dev:
         rc = fn(*args, st)
     else:

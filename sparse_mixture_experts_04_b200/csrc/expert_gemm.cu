@@ -152,7 +152,8 @@ constexpr int kI8StageBytes = 8 * 2048;
 template <int EPI, int BN, int STAGES>
 constexpr int gemm_smem_bytes() {
   return STAGES * TileCfg<EPI, BN>::kStageBytes + 256 /*barriers + flags*/ + 8 * (kMaxGroups + 1) +
-         (EPI == EPI_F32 ? kF32StageBytes + 16 : is_i8(EPI) ? kI8ScaleBytes + kI8StageBytes + 16 : 0) + 1024 /*alignment slack*/;
+         (EPI == EPI_F32 ? kF32StageBytes + 16 : is_i8(EPI) ? kI8ScaleBytes + kI8StageBytes + 16 : 0) +
+         1024 /*alignment slack*/;
 }
 
 struct TileInfo {
@@ -622,9 +623,18 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
       int stage = 0;
       uint32_t phase = 0, issued = 0, last_par = 0;
       bool ok = true;
+      // 8-bit products decode the next tile behind the first k-block of the
+      // current one, in time that the thread would wait for a free stage: a tile
+      // takes half of BF16's time, and the 1000 cycles of a decode between two
+      // tiles show (65536 rows, K = 2048: 443 -> 429 us).  BF16 gained nothing
+      // (the skewed layer lost 3%) and decodes when it needs the tile.
+      TileInfo next{};
+      if (is_i8(EPI) && static_cast<int>(blockIdx.x) < total_tiles)
+        next = decode_mixed_tile<kBM>(blockIdx.x, tiles1, total_tiles, prefix, prefix2, args, args2, C::kOutCols);
       for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
-        const TileInfo ti = decode_mixed_tile<kBM>(tile, tiles1, total_tiles, prefix, prefix2, args, args2,
-                                                   C::kOutCols);
+        const TileInfo ti = is_i8(EPI) ? next
+                                       : decode_mixed_tile<kBM>(tile, tiles1, total_tiles, prefix, prefix2, args,
+                                                                args2, C::kOutCols);
         const GemmArgs& A = ti.second ? args2 : args;
         const CUtensorMap* mA = ti.second ? &tmA_2 : &tmA;
         const CUtensorMap* mB = ti.second ? &tmB_2 : &tmB;
@@ -650,6 +660,9 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
           } else {
             tma_load_3d(b_dst, mB, &full[stage], kk, 0, 0);
           }
+          if (is_i8(EPI) && kb == 0 && tile + static_cast<int>(gridDim.x) < total_tiles)
+            next = decode_mixed_tile<kBM>(tile + gridDim.x, tiles1, total_tiles, prefix, prefix2, args, args2,
+                                          C::kOutCols);
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) {
@@ -672,11 +685,15 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
       uint32_t phase = 0;
       bool ok = test_stall(drain, abort_flag, args.stall_ns);
       int it = 0;
+      TileInfo next{};  // decoded ahead, as the copies' side does
+      if (is_i8(EPI) && static_cast<int>(blockIdx.x) < total_tiles)
+        next = decode_mixed_tile<kBM>(blockIdx.x, tiles1, total_tiles, prefix, prefix2, args, args2, C::kOutCols);
       for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x, ++it) {
         const int acc = it & 1;
         const uint32_t acc_par = static_cast<uint32_t>(it >> 1) & 1u;
-        const TileInfo ti = decode_mixed_tile<kBM>(tile, tiles1, total_tiles, prefix, prefix2, args, args2,
-                                                   C::kOutCols);
+        const TileInfo ti = is_i8(EPI) ? next
+                                       : decode_mixed_tile<kBM>(tile, tiles1, total_tiles, prefix, prefix2, args,
+                                                                args2, C::kOutCols);
         int k0, nkb;
         tile_k_range(ti.second ? args2 : args, ti.g, &k0, &nkb);
         if (!mbar_wait(&tempty[acc], acc_par ^ 1u, abort_flag)) {
@@ -701,6 +718,9 @@ __global__ void __launch_bounds__(gemm_threads(EPI), 1)
               umma_bf16(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, (kb | k) != 0 ? 1u : 0u);
           }
           umma_commit(&empty[stage]);
+          if (is_i8(EPI) && kb == 0 && tile + static_cast<int>(gridDim.x) < total_tiles)
+            next = decode_mixed_tile<kBM>(tile + gridDim.x, tiles1, total_tiles, prefix, prefix2, args, args2,
+                                          C::kOutCols);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -1077,8 +1097,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
       int stage = 0;
       uint32_t phase = 0, issued = 0, last_par = 0;
       bool ok = true;
+      // 8-bit products: the next tile decoded ahead (see the single-CTA kernel)
+      TileInfo next{};
+      if (is_i8(EPI) && pair < total_tiles)
+        next = decode_pair_tile(pair, tiles1, total_tiles, prefix, prefix2, args, args2, kOutCols);
       for (int tile = pair; ok && tile < total_tiles; tile += n_pairs) {
-        const TileInfo ti = decode_pair_tile(tile, tiles1, total_tiles, prefix, prefix2, args, args2, kOutCols);
+        const TileInfo ti = is_i8(EPI) ? next
+                                       : decode_pair_tile(tile, tiles1, total_tiles, prefix, prefix2, args, args2,
+                                                          kOutCols);
         const GemmArgs& A = ti.second ? args2 : args;
         const CUtensorMap* mA = ti.second ? &tmA_2 : &tmA;
         const CUtensorMap* mB = ti.second ? &tmB_2 : &tmB;
@@ -1144,6 +1170,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
               }
             }
           }
+          if (is_i8(EPI) && kb == 0 && tile + n_pairs < total_tiles)
+            next = decode_pair_tile(tile + n_pairs, tiles1, total_tiles, prefix, prefix2, args, args2, kOutCols);
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == kPairStages) {
@@ -1171,8 +1199,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
       uint32_t phase = 0;
       bool ok = true;
       int it = 0;
+      TileInfo next{};
+      if (is_i8(EPI) && pair < total_tiles)
+        next = decode_pair_tile(pair, tiles1, total_tiles, prefix, prefix2, args, args2, kOutCols);
       for (int tile = pair; ok && tile < total_tiles; tile += n_pairs, ++it) {
-        const TileInfo ti = decode_pair_tile(tile, tiles1, total_tiles, prefix, prefix2, args, args2, kOutCols);
+        const TileInfo ti = is_i8(EPI) ? next
+                                       : decode_pair_tile(tile, tiles1, total_tiles, prefix, prefix2, args, args2,
+                                                          kOutCols);
         const int a_box = ti.swap ? swap_box_rows(swap_n<EPI>(ti.row_end - ti.row0) / 2) : 128;
         const int kc = pair_tile_kc(ti.second ? args2 : args, ti, a_box);
         const int nkb = pair_nkb(ti.second ? args2 : args, kc);
@@ -1214,6 +1247,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI), 1
             }
           }
           umma_commit_pair_multicast(&empty[stage], 0x3);
+          if (is_i8(EPI) && kb == 0 && tile + n_pairs < total_tiles)
+            next = decode_pair_tile(tile + n_pairs, tiles1, total_tiles, prefix, prefix2, args, args2, kOutCols);
           if (++stage == kPairStages) {
             stage = 0;
             phase ^= 1u;
