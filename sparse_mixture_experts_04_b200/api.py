@@ -391,18 +391,24 @@ def moe_matmul_i8(x_q, x_scale, seg_off, w, w_scale, y, ws, stream=None):
     and [N] with seg_off None: every row); y [n_rows, N] BF16 or FP32; ws from
     alloc_matmul_workspace."""
     dev = _cuda("x_q", x_q)
-    wshape = w.shape
-    if len(wshape) not in (2, 3) or x_q.dim() != 2:
+    xshape, wshape, ydt = x_q.shape, w.shape, y.dtype
+    if len(wshape) not in (2, 3) or len(xshape) != 2:
         raise ValueError("x_q must be [n_rows, K] and w [G, N, K] or [N, K]")
-    G, N, K = wshape if len(wshape) == 3 else (1, *wshape)
-    rows, out = len(x_q), _ACT_CODE.get(y.dtype)
+    rows = xshape[0]
+    if len(wshape) == 3:
+        G, N, K = wshape
+        scale_shape = (G, N)
+    else:
+        G, (N, K) = 1, wshape
+        scale_shape = (N,)
+    out = _ACT_CODE.get(ydt)
     if out is None:
-        raise ValueError(f"y must be BF16 or FP32, got {y.dtype}")
+        raise ValueError(f"y must be BF16 or FP32, got {ydt}")
     _need("x_q", x_q, (rows, K), torch.int8, dev)
     _need("x_scale", x_scale, (rows,), torch.float32, dev)
     _need("w", w, wshape, torch.int8, dev)
-    _need("w_scale", w_scale, wshape[:-1], torch.float32, dev)
-    _need("y", y, (rows, N), y.dtype, dev)
+    _need("w_scale", w_scale, scale_shape, torch.float32, dev)
+    _need("y", y, (rows, N), ydt, dev)
     _need_ws(ws, dev)
     if seg_off is not None:
         _need("seg_off", seg_off, (G + 1,), torch.int32, dev)
