@@ -250,16 +250,19 @@ struct Few : FewTile<WT> {
   // token groups of the shared experts / of the routed ones, for rows per group ng
   __device__ __forceinline__ int shared_groups(int ng) const { return (a.T + ng - 1) / ng; }
 
-  // units of a pass
-  __device__ __forceinline__ int64_t units(int pass) const {
-    if (pass == kUpShared) return static_cast<int64_t>(a.Ns) * shared_groups(a.ng_up) * nfb;
-    if (pass == kUpRouted) return static_cast<int64_t>(s.groups[0][a.E]) * nfb;
-    if (pass == kDownShared) return static_cast<int64_t>(a.Ns) * a.nc * shared_groups(a.ng_down) * nb;
-    return static_cast<int64_t>(s.groups[1][a.E]) * a.nc * nb;
+  // units of a pass (fewer than 2^31: few_supported)
+  __device__ __forceinline__ unsigned units(int pass) const {
+    const bool up = pass <= kUpRouted;
+    const unsigned groups = pass == kUpRouted || pass == kDownRouted
+                                ? s.groups[up ? 0 : 1][a.E]
+                                : static_cast<unsigned>(a.Ns) * shared_groups(up ? a.ng_up : a.ng_down);
+    return groups * static_cast<unsigned>(up ? nfb : a.nc * nb);
   }
+  // this CTA's: n / n_cta of them, the first n % n_cta CTAs one more
   __device__ __forceinline__ PassRange range(int pass) const {
-    const int64_t n = units(pass);
-    return PassRange{static_cast<int>(n * cta / n_cta), static_cast<int>(n * (cta + 1) / n_cta)};
+    const unsigned n = units(pass), each = n / n_cta, more = n - each * n_cta;
+    const unsigned first = cta * each + min(static_cast<unsigned>(cta), more);
+    return PassRange{static_cast<int>(first), static_cast<int>(first + each + (cta < static_cast<int>(more) ? 1 : 0))};
   }
 
   // expert of routed token group v (largest e with groups[e] <= v that has groups)
@@ -1100,11 +1103,13 @@ __global__ void __launch_bounds__(FewTile<WT>::kThreads, 1) few_layer_kernel(con
   }
   __syncthreads();
   if (worker) {
-    few_pass(f, kUpShared, used, red, n_units, held, tid);
-    few_pass(f, kUpRouted, used, red, n_units, held, tid);
-    few_grid_sync(a.arrivals + 1, &s.abort_flag, tid);
-    few_pass(f, kDownShared, used, red, n_units, held, tid);
-    few_pass(f, kDownRouted, used, red, n_units, held, tid);
+    // one copy of the code for all passes: what runs for the first time is
+    // fetched from memory first (the weights' stream evicts it between calls)
+#pragma unroll 1
+    for (int pass = 0; pass < kPasses; ++pass) {
+      if (pass == kDownShared) few_grid_sync(a.arrivals + 1, &s.abort_flag, tid);
+      few_pass(f, pass, used, red, n_units, held, tid);
+    }
     // the gates and slots of the combine, while the other CTAs finish
     named_bar_sync(1, kFewWorkers);
     int32_t* slot = reinterpret_cast<int32_t*>(tok);
