@@ -242,20 +242,19 @@ struct Few : FewTile<WT> {
   uint8_t* ring;
   uint8_t* tok;
   int cta, n_cta, nfb, nb;
+  int sg_up, sg_down;  // token groups of a shared expert
 
   __device__ __forceinline__ Few(const FewArgs& a_, FewShared& s_, uint8_t* ring_, uint8_t* tok_)
       : a(a_), s(s_), ring(ring_), tok(tok_), cta(blockIdx.x), n_cta(gridDim.x), nfb(a_.F / 8),
-        nb((a_.d + kFewRows - 1) / kFewRows) {}
-
-  // token groups of the shared experts / of the routed ones, for rows per group ng
-  __device__ __forceinline__ int shared_groups(int ng) const { return (a.T + ng - 1) / ng; }
+        nb((a_.d + kFewRows - 1) / kFewRows), sg_up((a_.T + a_.ng_up - 1) / a_.ng_up),
+        sg_down((a_.T + a_.ng_down - 1) / a_.ng_down) {}
 
   // units of a pass (fewer than 2^31: few_supported)
   __device__ __forceinline__ unsigned units(int pass) const {
     const bool up = pass <= kUpRouted;
     const unsigned groups = pass == kUpRouted || pass == kDownRouted
                                 ? s.groups[up ? 0 : 1][a.E]
-                                : static_cast<unsigned>(a.Ns) * shared_groups(up ? a.ng_up : a.ng_down);
+                                : static_cast<unsigned>(a.Ns) * (up ? sg_up : sg_down);
     return groups * static_cast<unsigned>(up ? nfb : a.nc * nb);
   }
   // this CTA's: n / n_cta of them, the first n % n_cta CTAs one more
@@ -265,14 +264,13 @@ struct Few : FewTile<WT> {
     return PassRange{static_cast<int>(first), static_cast<int>(first + each + (cta < static_cast<int>(more) ? 1 : 0))};
   }
 
-  // expert of routed token group v (largest e with groups[e] <= v that has groups)
+  // expert of routed token group v: the last e with groups[e] <= v, by counting
+  // (whole warps; a binary search is seven dependent loads)
   __device__ __forceinline__ int group_expert(const int* groups, int v) const {
-    int lo = 0, hi = a.E - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (groups[mid] <= v) lo = mid; else hi = mid - 1;
-    }
-    return lo;
+    int n = 0;
+#pragma unroll 1
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) n += groups[e] <= v ? 1 : 0;
+    return __reduce_add_sync(0xffffffffu, n) - 1;
   }
 
   // The span that unit u begins or lies in: its units share tokens, expert and
@@ -286,15 +284,15 @@ struct Few : FewTile<WT> {
     const int blk = u - v * per;
     q.units = min(per - blk, last - u);
     q.c = 0;
-    if (!up) {
+    if (!up && a.nc > 1) {
       const int t = v;
       v = t / a.nc;
       q.c = t - v * a.nc;
     }
     const char* base;
     if (pass == kUpShared || pass == kDownShared) {
-      const int sg = shared_groups(ng);
-      q.e = v / sg;
+      const int sg = up ? sg_up : sg_down;
+      q.e = sg == 1 ? v : v / sg;
       q.row0 = (v - q.e * sg) * ng;
       q.n = min(ng, a.T - q.row0);
       base = up ? a.w13_s : a.w2_s;
@@ -324,6 +322,26 @@ struct Few : FewTile<WT> {
       q.w = base + (static_cast<int64_t>(q.e) * a.d + q.col) * q.row_bytes + k0;
     }
     return q;
+  }
+};
+
+// A place in the CTA's list of units: the units of a pass, then those of the next.
+template <int WT>
+struct Place {
+  int pass, u, last;
+  __device__ __forceinline__ Place(const Few<WT>& f, int first_pass) : pass(first_pass) { enter(f); }
+  __device__ __forceinline__ void enter(const Few<WT>& f) {
+    const PassRange r = f.range(pass);
+    u = r.first;
+    last = r.last;
+  }
+  // whether a unit is left in the pass or, entering it, in the routed pass after it
+  __device__ __forceinline__ bool more(const Few<WT>& f) {
+    if (u >= last && (pass == kUpShared || pass == kDownShared)) {
+      ++pass;
+      enter(f);
+    }
+    return u < last;
   }
 };
 
@@ -409,12 +427,14 @@ template <int WT>
 struct FewMathMma {
   using Acc = typename Few<WT>::Acc;
   static constexpr int kWarps = Few<WT>::kTeamWarps, kChunk = FewTile<WT>::kChunk, kPitch = FewTile<WT>::kPitch;
-  Acc acc[2][4];
+  // [token tile][chain]: two chains of dependent products instead of one twice
+  // as long
+  Acc acc[2][2][4];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = 0;
+      for (int i = 0; i < 4; ++i) acc[j >> 1][j & 1][i] = 0;
   }
   // w: the stage; t: the token buffer at the stage's first byte of the rows
   __device__ __forceinline__ void stage(const uint8_t* w, const uint8_t* t, int t_pitch, int cb, int n_tok, int rows,
@@ -433,12 +453,12 @@ struct FewMathMma {
         ldmatrix_x4(wa + o, a0);
         ldmatrix_x4(wa + o + 32, a1);
         ldmatrix_x4(ta + o, b);
-        mma_16x8(acc[0], a0, b[0], b[1]);
-        mma_16x8(acc[0], a1, b[2], b[3]);
+        mma_16x8(acc[0][0], a0, b[0], b[1]);
+        mma_16x8(acc[0][1], a1, b[2], b[3]);
         if (n_tok > 8) {
           ldmatrix_x4(tb + o, b);
-          mma_16x8(acc[1], a0, b[0], b[1]);
-          mma_16x8(acc[1], a1, b[2], b[3]);
+          mma_16x8(acc[1][0], a0, b[0], b[1]);
+          mma_16x8(acc[1][1], a1, b[2], b[3]);
         }
       }
       return;
@@ -454,12 +474,12 @@ struct FewMathMma {
       }
       if (rows == 8) a0[1] = a0[3] = a1[1] = a1[3] = 0;
       ldmatrix_x4(ta + o, b);
-      mma_16x8(acc[0], a0, b[0], b[1]);
-      mma_16x8(acc[0], a1, b[2], b[3]);
+      mma_16x8(acc[0][0], a0, b[0], b[1]);
+      mma_16x8(acc[0][1], a1, b[2], b[3]);
       if (n_tok > 8) {
         ldmatrix_x4(tb + o, b);
-        mma_16x8(acc[1], a0, b[0], b[1]);
-        mma_16x8(acc[1], a1, b[2], b[3]);
+        mma_16x8(acc[1][0], a0, b[0], b[1]);
+        mma_16x8(acc[1][1], a1, b[2], b[3]);
       }
     }
   }
@@ -469,10 +489,10 @@ struct FewMathMma {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (j * 8 >= n_tok) break;
-      r[j * 128] = acc[j][0];
-      r[j * 128 + 1] = acc[j][1];
-      r[j * 128 + 64] = acc[j][2];
-      r[j * 128 + 65] = acc[j][3];
+      r[j * 128] = acc[j][0][0] + acc[j][1][0];
+      r[j * 128 + 1] = acc[j][0][1] + acc[j][1][1];
+      r[j * 128 + 64] = acc[j][0][2] + acc[j][1][2];
+      r[j * 128 + 65] = acc[j][0][3] + acc[j][1][3];
     }
   }
   __device__ __forceinline__ static Acc get(const void* red, int row, int tok) {
@@ -551,21 +571,31 @@ struct FewMath<kFewF32> {
 };
 
 // ---------------------------------------------------------------- token rows
-// What the token buffer holds: the same rows need no second load (one token:
-// every expert; the shared experts: every group).
-__device__ __forceinline__ int few_token_key(const FewArgs& a, const FewShared& s, int pass, const Span& q) {
-  if (pass > kUpRouted) return -1;
-  if (q.n == 1) return pass == kUpRouted ? s.perm[q.row0] / a.K : q.row0;
-  return pass == kUpShared ? (q.n << 16 | q.row0) : -1;
+// What the token buffer holds: the same rows need no second load (the shared
+// experts: every group; one token: every expert's up product).
+__device__ __forceinline__ int few_token_key(const FewArgs& a, int pass, const Span& q) {
+  if (pass == kUpRouted && a.T == 1) return 1 << 16;
+  return pass == kUpShared ? q.n << 16 | q.row0 : -1;
 }
+
+// distance of the rows in the token buffer: whole 64-byte slices, and an odd
+// number of 16-byte pieces against bank conflicts
+__device__ __forceinline__ int few_token_pitch(int len) { return ((len + 63) & ~63) + 16; }
 
 // Rows of the span's group into the token buffer, zero behind the row's end up
 // to the next multiple of 64 bytes.  up: rows of x (8-bit weights: its integers
 // from step 1); down: a chunk of hidden rows (8-bit weights: FP32, rounded to
 // integers here; every CTA has contributed to the row's largest magnitude).
-// Four 16-byte pieces per thread are in flight.
+// tok, row_scale: the span's first row and scale.  Rows that need no rounding
+// are copied asynchronously: the caller waits.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {  // the rest of 16: zero
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 template <int WT>
-__device__ __forceinline__ void few_load_tokens(const Few<WT>& f, int pass, const Span& q, int t_pitch, int tid) {
+__device__ __forceinline__ void few_load_tokens(const Few<WT>& f, int pass, const Span& q, uint8_t* tok,
+                                                float* row_scale, int t_pitch, int tid) {
   const FewArgs& a = f.a;
   const bool up = pass <= kUpRouted;
   const bool routed = pass == kUpRouted || pass == kDownRouted;
@@ -583,21 +613,14 @@ __device__ __forceinline__ void few_load_tokens(const Few<WT>& f, int pass, cons
         src = static_cast<const char*>(routed ? a.h : a.h_s) +
               (routed ? q.row0 + r : static_cast<int64_t>(q.row0 + r) * a.Ns + q.e) * a.F * Few<WT>::kW +
               static_cast<int64_t>(q.c) * a.chunk_bytes;
-      uint8_t* dst = f.tok + r * t_pitch;
-      for (int v = v0; v < all; v += 4 * per) {
-        uint4 z[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          z[j] = make_uint4(0, 0, 0, 0);
-          if (v + j * per < vecs) z[j] = __ldcg(reinterpret_cast<const uint4*>(src) + v + j * per);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (v + j * per < all) *reinterpret_cast<uint4*>(dst + (v + j * per) * 16) = z[j];
+      const uint32_t dst = smem_addr(tok + r * t_pitch);
+      for (int v = v0; v < all; v += per) {
+        const bool in = v < vecs;
+        cp_async16(dst + v * 16, src + (in ? v * 16 : 0), in ? 16 : 0);
       }
     }
     if (WT == kFewI8 && tid < q.n)
-      f.s.row_scale[tid] = __ldcg(a.x_scale + (routed ? f.s.perm[q.row0 + tid] / a.K : q.row0 + tid));
+      row_scale[tid] = __ldcg(a.x_scale + (routed ? f.s.perm[q.row0 + tid] / a.K : q.row0 + tid));
   } else {
     if (r >= q.n) return;
     const int64_t row = q.row0 + r;
@@ -621,8 +644,8 @@ __device__ __forceinline__ void few_load_tokens(const Few<WT>& f, int pass, cons
           w[j] = quant_pack4(e, scale, inv);
         }
       }
-      *reinterpret_cast<uint4*>(f.tok + r * t_pitch + v * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (v == 0) f.s.row_scale[r] = scale;
+      *reinterpret_cast<uint4*>(tok + r * t_pitch + v * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (v == 0) row_scale[r] = scale;
     }
   }
 }
@@ -684,7 +707,7 @@ __device__ __forceinline__ float2 few_scales(const Few<WT>& f, int pass, const S
 // sc: few_scales of this unit
 template <int WT>
 __device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const Span& q, const void* red, float2 sc,
-                                               int tid) {
+                                               const float* row_scale, int tid) {
   using M = FewMath<WT>;
   const FewArgs& a = f.a;
   if (pass <= kUpRouted) {  // 8 features x n tokens: lane groups of 8 share a token
@@ -693,7 +716,7 @@ __device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const
     float h = 0.f;
     if (live) {
       if constexpr (WT == kFewI8) {
-        const float sx = f.s.row_scale[tok];
+        const float sx = row_scale[tok];
         const float g = __int2float_rn(M::get(red, ft, tok)) * (sx * sc.x);
         const float u = __int2float_rn(M::get(red, ft + 8, tok)) * (sx * sc.y);
         h = silu(g) * u;
@@ -721,7 +744,7 @@ __device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const
     for (int tok = tid >> 4; tok < q.n; tok += Few<WT>::kTeamWarps * 2) {
       float v;
       if constexpr (WT == kFewI8)
-        v = __int2float_rn(M::get(red, n, tok)) * (f.s.row_scale[tok] * sc.x);
+        v = __int2float_rn(M::get(red, n, tok)) * (row_scale[tok] * sc.x);
       else
         v = M::get(red, n, tok);
       const int64_t row = q.row0 + tok;
@@ -733,30 +756,58 @@ __device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const
   }
 }
 
-// All units of one pass that are this CTA's (the 256 worker threads).  Team t
-// takes units t, t + teams, ... of a span; `used`: stages this team has consumed.
+// All units of two passes, first_pass (shared experts) and the next (routed
+// ones), that are this CTA's (the 256 worker threads).  Team t takes units t,
+// t + teams, ... of a span; `used`: stages this team has consumed.
 template <int WT>
-__device__ __forceinline__ void few_pass(const Few<WT>& f, int pass, uint32_t& used, uint8_t* red_base,
-                                         uint32_t& n_units, int& held, int tid) {
+__device__ __forceinline__ void few_passes(const Few<WT>& f, int first_pass, uint32_t& used, uint8_t* red_base,
+                                           uint32_t& n_units, int& held, int tid) {
   constexpr int kTeams = Few<WT>::kTeams, kWarps = Few<WT>::kTeamWarps, kSlots = kFewStages / kTeams;
   constexpr int kChunk = Few<WT>::kChunk;
   const int lane = tid & 31, team = (tid >> 5) / kWarps, warp = (tid >> 5) % kWarps;
-  const PassRange r = f.range(pass);
   FewMath<WT> math;
   red_base += team * (kFewRedBytes / kTeams);
-  for (int u = r.first; u < r.last;) {
-    Span q = f.span(pass, u, r.last);
-    u += q.units;
-    const int t_pitch = ((q.len + 63) & ~63) + 16;
-    const int key = few_token_key(f.a, f.s, pass, q);
-    if (key < 0 || key != held) {
-      // the last unit's reads of the token buffer (and of the row scales) are
-      // over only once its outputs are stored
-      named_bar_sync(1, kFewWorkers);
-      few_load_tokens(f, pass, q, t_pitch, tid);
-      named_bar_sync(1, kFewWorkers);
-      held = key;
+  Place<WT> here(f, first_pass);
+  int loaded = 0;           // spans, from this one on, whose rows are in the token buffer,
+  int at = 0, row = 0;      // the next one's at byte `at`, their scales at `row`
+  while (here.more(f)) {
+    Span q = f.span(here.pass, here.u, here.last);
+    const int pass = here.pass, t_pitch = few_token_pitch(q.len);
+    here.u += q.units;
+    if (loaded == 0) {
+      at = row = 0;
+      loaded = 1;
+      const int key = few_token_key(f.a, pass, q);
+      if (key < 0 || key != held) {
+        // the last unit's reads of the token buffer (and of the row scales) are
+        // over only once its outputs are stored
+        named_bar_sync(1, kFewWorkers);
+        // with as many of the next spans' rows as fit: a load costs 1.5 us of
+        // latency and barriers
+        Place<WT> p = here;
+        Span n = q;
+        int bytes = 0, rows = 0;
+        for (;;) {
+          const int pitch = few_token_pitch(n.len);
+          few_load_tokens(f, p.pass, n, f.tok + bytes, f.s.row_scale + rows, pitch, tid);
+          bytes += n.n * pitch;
+          rows += n.n;
+          if (key >= 0 || !p.more(f)) break;
+          n = f.span(p.pass, p.u, p.last);
+          if (rows + n.n > 16 || bytes + n.n * few_token_pitch(n.len) > Few<WT>::kTokBytes) break;
+          p.u += n.units;
+          ++loaded;
+        }
+        cp_async_wait_all();
+        named_bar_sync(1, kFewWorkers);
+        held = key;
+      }
     }
+    --loaded;
+    const uint8_t* tok = f.tok + at;
+    const float* row_scale = f.s.row_scale + row;
+    at += q.n * t_pitch;
+    row += q.n;
     q.col += team * q.step;
     // 8-bit weights: the scales are fetched one unit ahead (fetched when needed
     // they cost the team a memory latency per unit: 210 -> 200 us for 7 tokens
@@ -773,14 +824,14 @@ __device__ __forceinline__ void few_pass(const Few<WT>& f, int pass, uint32_t& u
         const int slot = team * kSlots + static_cast<int>(used % kSlots);
         mbar_wait(&f.s.full[slot], (used / kSlots) & 1u, &f.s.abort_flag);
         __syncwarp();
-        math.stage(f.ring + slot * Few<WT>::kStageBytes, f.tok + off, t_pitch, min(kChunk, q.len - off), q.n, rows,
+        math.stage(f.ring + slot * Few<WT>::kStageBytes, tok + off, t_pitch, min(kChunk, q.len - off), q.n, rows,
                    warp, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&f.s.empty[slot]);
       }
       math.put(red, q.n, warp, lane);
       named_bar_sync(2 + team, kWarps * 32);  // the unit's sums are complete
-      few_store_unit(f, pass, q, red, sc, team_tid);
+      few_store_unit(f, pass, q, red, sc, row_scale, team_tid);
       q.col += kTeams * q.step;
       ++n_units;  // the next unit's sums go to the other half: no barrier before they are written
     }
@@ -1086,29 +1137,27 @@ __global__ void __launch_bounds__(FewTile<WT>::kThreads, 1) few_layer_kernel(con
   if (worker) {
     int32_t* idx = reinterpret_cast<int32_t*>(tok);
     const bool write = blockIdx.x == 0;
+    float* w = reinterpret_cast<float*>(tok) + kFewMaxPairs;
+    // (one call: the code of two would be fetched from memory twice as often)
+    few_select_any(a, s, a.spread ? a.topk_idx : idx, a.spread ? a.topk_w : w, a.stats && (a.spread || write),
+                   a.spread ? blockIdx.x + warp * gridDim.x : warp, (a.spread ? gridDim.x : 1) * (kFewWorkers / 32),
+                   lane);
     if (a.spread) {
-      few_select_any(a, s, a.topk_idx, a.topk_w, a.stats != nullptr, blockIdx.x + warp * gridDim.x,
-                     gridDim.x * (kFewWorkers / 32), lane);
       few_grid_sync(a.arrivals, &s.abort_flag, tid);
 #pragma unroll 1
       for (int i = tid; i < a.T * a.K; i += kFewWorkers) idx[i] = __ldcg(a.topk_idx + i);
-      named_bar_sync(1, kFewWorkers);
-      few_dispatch(a, s, idx, nullptr, write, tid);
-    } else {
-      float* w = reinterpret_cast<float*>(tok) + kFewMaxPairs;
-      few_select_any(a, s, idx, w, write && a.stats, warp, kFewWorkers / 32, lane);
-      named_bar_sync(1, kFewWorkers);
-      few_dispatch(a, s, idx, w, write, tid);
     }
+    named_bar_sync(1, kFewWorkers);
+    few_dispatch(a, s, idx, a.spread ? nullptr : w, write, tid);
   }
   __syncthreads();
   if (worker) {
     // one copy of the code for all passes: what runs for the first time is
     // fetched from memory first (the weights' stream evicts it between calls)
 #pragma unroll 1
-    for (int pass = 0; pass < kPasses; ++pass) {
+    for (int pass = kUpShared; pass <= kDownShared; pass += kDownShared - kUpShared) {
       if (pass == kDownShared) few_grid_sync(a.arrivals + 1, &s.abort_flag, tid);
-      few_pass(f, pass, used, red, n_units, held, tid);
+      few_passes(f, pass, used, red, n_units, held, tid);
     }
     // the gates and slots of the combine, while the other CTAs finish
     named_bar_sync(1, kFewWorkers);
