@@ -16,9 +16,9 @@ namespace moe {
 
 constexpr int kQuantThreads = 256;
 
-// One block per row.  A thread keeps up to kQuantKeep 16-element pieces of its
-// row in registers between the maximum and the rounding; longer rows are read
-// again (from L2).
+// Rows of more than 16384 BF16 or 8192 FP32 values: one block per row.  A thread keeps up to kQuantKeep
+// 16-element pieces of its row in registers between the maximum and the rounding;
+// the rest is read again (from L2).
 constexpr int kQuantKeep = 2;
 
 template <typename T>
@@ -109,74 +109,74 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const T* _
   }
 }
 
-// One warp per row, for many rows: all loads of a chunk (8 vectors of 16 bytes
-// per lane) in flight and no block barrier.  A row of one chunk stays packed in
-// registers between the maximum and the rounding; longer ones are read again,
-// from L2.  (A block per row took 150 us for 65536 rows of 2048 BF16: two
-// barriers and a mostly idle block per 4 KB.  A warp per row: 74 us, 402 MB.)
+// W warps per row: the row's loads (kQuantVecs vectors of 16 bytes per lane) all
+// in flight, the row in registers between the maximum and the rounding, at most
+// one barrier of W warps.  W is the fewest that hold the row, more while the SMs
+// have fewer than 8 warps each (600 rows of 2048 BF16: 2.8 us; with at most 4 or
+// up to 16 warps an SM 3.3 and 3.1).  Copy bandwidth for large calls: 65536 rows of
+// 2048 BF16 60.8 us (402 MB, 6.6 TB/s), 9600 of 8192 38.0 us (236 MB, 6.2 TB/s); a
+// block per row 165 and 52 us.
 constexpr int kQuantVecs = 8;
+constexpr int kQuantWarps = 8;
 
-template <typename T>
-__device__ __forceinline__ void load_chunk(const uint4* xr, int first, int vecs, int lane, uint4 (&v)[kQuantVecs]) {
-#pragma unroll
-  for (int i = 0; i < kQuantVecs; ++i) {
-    const int at = first + lane + i * 32;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (at < vecs) v[i] = __ldg(xr + at);
-  }
-}
-
-template <typename T>
+template <typename T, int W>
 __global__ void __launch_bounds__(kQuantThreads, 4) quantize_rows_warp_kernel(const T* __restrict__ x, int64_t n_rows,
                                                                               int n_cols, int8_t* __restrict__ q,
                                                                               float* __restrict__ scale) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));  // elements of a vector
-  constexpr int kChunk = 32 * kQuantVecs;              // vectors of a chunk
+  constexpr int kTeams = kQuantThreads / 32 / W;       // rows of a block
+  __shared__ unsigned s_max[2][kQuantThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, vecs = n_cols / V;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32);
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5); row < n_rows;
-       row += warps) {
+  const int warp = threadIdx.x >> 5, team = warp / W, vecs = n_cols / V;
+  const int lane = threadIdx.x - team * W * 32;  // of the row's 32 W
+  int turn = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kTeams + team; row < n_rows;
+       row += static_cast<int64_t>(gridDim.x) * kTeams, turn ^= 1) {
     const uint4* xr = reinterpret_cast<const uint4*>(x + row * n_cols);
     uint4 v[kQuantVecs];
+#pragma unroll
+    for (int i = 0; i < kQuantVecs; ++i) {
+      const int at = lane + i * 32 * W;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (at < vecs) v[i] = __ldg(xr + at);
+    }
     unsigned m = 0;
-#pragma unroll 1
-    for (int first = 0; first < vecs; first += kChunk) {
-      load_chunk<T>(xr, first, vecs, lane, v);
 #pragma unroll
-      for (int i = 0; i < kQuantVecs; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    for (int i = 0; i < kQuantVecs; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (sizeof(T) == 2)  // the magnitudes' bits of two BF16 order as 16-bit integers
-            m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
-          else
-            m = max(m, w[j] & 0x7FFFFFFFu);
-        }
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 2)  // the magnitudes' bits of two BF16 order as 16-bit integers
+          m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+        else
+          m = max(m, w[j] & 0x7FFFFFFFu);
       }
     }
     if constexpr (sizeof(T) == 2) m = max(m & 0xFFFF0000u, m << 16);
-    const float s = quant_scale(warp_max_u32(m));
+    m = warp_max_u32(m);
+    if constexpr (W > 1) {
+      if ((threadIdx.x & 31) == 0) s_max[turn][warp] = m;
+      named_bar_sync(1 + team, W * 32);
+#pragma unroll
+      for (int w = 0; w < W; ++w) m = max(m, s_max[turn][team * W + w]);
+    }
+    const float s = quant_scale(m);
     const float inv = 1.0f / s;
     int8_t* qr = q + row * n_cols;
-#pragma unroll 1
-    for (int first = 0; first < vecs; first += kChunk) {
-      if (vecs > kChunk) load_chunk<T>(xr, first, vecs, lane, v);
 #pragma unroll
-      for (int i = 0; i < kQuantVecs; ++i) {
-        const int at = first + lane + i * 32;
-        if (at < vecs) {
-          if constexpr (sizeof(T) == 2) {
-            const float lo[4] = {bf16_lo(v[i].x), bf16_hi(v[i].x), bf16_lo(v[i].y), bf16_hi(v[i].y)};
-            const float hi[4] = {bf16_lo(v[i].z), bf16_hi(v[i].z), bf16_lo(v[i].w), bf16_hi(v[i].w)};
-            *reinterpret_cast<uint2*>(qr + static_cast<int64_t>(at) * 8) =
-                make_uint2(quant_pack4(lo, s, inv), quant_pack4(hi, s, inv));
-          } else {
-            const float f[4] = {__uint_as_float(v[i].x), __uint_as_float(v[i].y), __uint_as_float(v[i].z),
-                                __uint_as_float(v[i].w)};
-            *reinterpret_cast<uint32_t*>(qr + static_cast<int64_t>(at) * 4) = quant_pack4(f, s, inv);
-          }
+    for (int i = 0; i < kQuantVecs; ++i) {
+      const int at = lane + i * 32 * W;
+      if (at < vecs) {
+        if constexpr (sizeof(T) == 2) {
+          const float lo[4] = {bf16_lo(v[i].x), bf16_hi(v[i].x), bf16_lo(v[i].y), bf16_hi(v[i].y)};
+          const float hi[4] = {bf16_lo(v[i].z), bf16_hi(v[i].z), bf16_lo(v[i].w), bf16_hi(v[i].w)};
+          *reinterpret_cast<uint2*>(qr + static_cast<int64_t>(at) * 8) =
+              make_uint2(quant_pack4(lo, s, inv), quant_pack4(hi, s, inv));
+        } else {
+          const float f[4] = {__uint_as_float(v[i].x), __uint_as_float(v[i].y), __uint_as_float(v[i].z),
+                              __uint_as_float(v[i].w)};
+          *reinterpret_cast<uint32_t*>(qr + static_cast<int64_t>(at) * 4) = quant_pack4(f, s, inv);
         }
       }
     }
@@ -187,15 +187,20 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quantize_rows_warp_kernel(co
 template <typename T>
 static cudaError_t run_quantize_rows(const T* x, int64_t n_rows, int n_cols, int8_t* q, float* scale,
                                      cudaStream_t st) {
-  // a warp per row once the rows give every SM a few warps, for rows of several
-  // chunks many warps (600 rows of 8192: 37 us so, 13 us a block each); else a
-  // block per row
-  const bool one_chunk = n_cols <= kQuantVecs * 32 * 16 / static_cast<int>(sizeof(T));
-  if ((one_chunk && n_rows >= 4 * num_sms()) || (n_cols <= 8192 && n_rows >= 48 * num_sms())) {
-    int64_t grid = (n_rows + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
-    if (grid > 65536) grid = 65536;
-    return launch_k(quantize_rows_warp_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(kQuantThreads), 0, st, x,
-                    n_rows, n_cols, q, scale);
+  const int vecs = n_cols / (16 / static_cast<int>(sizeof(T)));
+  int w = 1;
+  while (w < 8 && (vecs > 32 * kQuantVecs * w || n_rows * w < kQuantWarps * num_sms())) w *= 2;
+  if (vecs <= 32 * kQuantVecs * w) {
+    const int teams = kQuantThreads / 32 / w;
+    const int64_t blocks = (n_rows + teams - 1) / teams;
+    const auto run = [&](auto kernel) {
+      return launch_k(kernel, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)), dim3(kQuantThreads), 0, st,
+                      x, n_rows, n_cols, q, scale);
+    };
+    if (w == 1) return run(quantize_rows_warp_kernel<T, 1>);
+    if (w == 2) return run(quantize_rows_warp_kernel<T, 2>);
+    if (w == 4) return run(quantize_rows_warp_kernel<T, 4>);
+    return run(quantize_rows_warp_kernel<T, 8>);
   }
   const unsigned grid = static_cast<unsigned>(n_rows < 65536 ? n_rows : 65536);
   return launch_k(quantize_rows_kernel<T>, dim3(grid), dim3(kQuantThreads), 0, st, x, n_rows, n_cols, q, scale);

@@ -36,6 +36,22 @@ def test_quantize_rows_equals_the_definition(rows, cols, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1250, 2032), (1250, 4112), (1250, 8208), (640, 528), (311, 1040), (160, 4000),
+                                       (70, 16400), (1, 8176), (5000, 1024)])
+def test_quantize_rows_for_every_number_of_warps_per_row(rows, cols, dt):
+    """Coarse values, so that ties are common; some rows all equal or zero."""
+    g = gen(rows + cols)
+    x = torch.randint(-64, 65, (rows, cols), generator=g).float() * 0.375
+    x[rows // 2] = 0.0
+    x[-1] = -2.5
+    x = x.to(DT[dt])
+    q, s = api.quantize_rows(x.cuda())
+    wq, ws = ref.quantize(x)
+    assert torch.equal(s.cpu().double(), ws)
+    assert torch.equal(q.cpu().double(), wq)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_quantize_rows_at_ties_and_extremes(dt):
     t = DT[dt]
     k = torch.arange(-127, 128).float()
