@@ -119,49 +119,62 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const T* _
 constexpr int kQuantVecs = 8;
 constexpr int kQuantWarps = 8;
 
+// The row's vectors of lane `lane` of its 32 W, and the largest magnitude's bits
+// over the row (turn: which half of s_max).
+template <typename T, int W>
+__device__ __forceinline__ unsigned load_row(const T* xr, int vecs, int lane, int team, unsigned (&s_max)[2][8],
+                                             int turn, uint4 (&v)[kQuantVecs]) {
+#pragma unroll
+  for (int i = 0; i < kQuantVecs; ++i) {
+    const int at = lane + i * 32 * W;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (at < vecs) v[i] = __ldg(reinterpret_cast<const uint4*>(xr) + at);
+  }
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < kQuantVecs; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 2)  // the magnitudes' bits of two BF16 order as 16-bit integers
+        m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+      else
+        m = max(m, w[j] & 0x7FFFFFFFu);
+    }
+  }
+  if constexpr (sizeof(T) == 2) m = max(m & 0xFFFF0000u, m << 16);
+  m = warp_max_u32(m);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 31) == 0) s_max[turn][threadIdx.x >> 5] = m;
+    named_bar_sync(1 + team, W * 32);
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = max(m, s_max[turn][team * W + w]);
+  }
+  return m;
+}
+
+// Eight BF16 to eight bytes.
+__device__ __forceinline__ uint2 quant_pack8(const uint4& v, float s, float inv) {
+  const float lo[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+  const float hi[4] = {bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
+  return make_uint2(quant_pack4(lo, s, inv), quant_pack4(hi, s, inv));
+}
+
 template <typename T, int W>
 __global__ void __launch_bounds__(kQuantThreads, 4) quantize_rows_warp_kernel(const T* __restrict__ x, int64_t n_rows,
                                                                               int n_cols, int8_t* __restrict__ q,
                                                                               float* __restrict__ scale) {
-  constexpr int V = 16 / static_cast<int>(sizeof(T));  // elements of a vector
-  constexpr int kTeams = kQuantThreads / 32 / W;       // rows of a block
+  constexpr int kTeams = kQuantThreads / 32 / W;  // rows of a block
   __shared__ unsigned s_max[2][kQuantThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, team = warp / W, vecs = n_cols / V;
+  const int team = (threadIdx.x >> 5) / W, vecs = n_cols / (16 / static_cast<int>(sizeof(T)));
   const int lane = threadIdx.x - team * W * 32;  // of the row's 32 W
   int turn = 0;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kTeams + team; row < n_rows;
        row += static_cast<int64_t>(gridDim.x) * kTeams, turn ^= 1) {
-    const uint4* xr = reinterpret_cast<const uint4*>(x + row * n_cols);
     uint4 v[kQuantVecs];
-#pragma unroll
-    for (int i = 0; i < kQuantVecs; ++i) {
-      const int at = lane + i * 32 * W;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (at < vecs) v[i] = __ldg(xr + at);
-    }
-    unsigned m = 0;
-#pragma unroll
-    for (int i = 0; i < kQuantVecs; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (sizeof(T) == 2)  // the magnitudes' bits of two BF16 order as 16-bit integers
-          m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
-        else
-          m = max(m, w[j] & 0x7FFFFFFFu);
-      }
-    }
-    if constexpr (sizeof(T) == 2) m = max(m & 0xFFFF0000u, m << 16);
-    m = warp_max_u32(m);
-    if constexpr (W > 1) {
-      if ((threadIdx.x & 31) == 0) s_max[turn][warp] = m;
-      named_bar_sync(1 + team, W * 32);
-#pragma unroll
-      for (int w = 0; w < W; ++w) m = max(m, s_max[turn][team * W + w]);
-    }
-    const float s = quant_scale(m);
+    const float s = quant_scale(load_row<T, W>(x + row * n_cols, vecs, lane, team, s_max, turn, v));
     const float inv = 1.0f / s;
     int8_t* qr = q + row * n_cols;
 #pragma unroll
@@ -169,10 +182,7 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quantize_rows_warp_kernel(co
       const int at = lane + i * 32 * W;
       if (at < vecs) {
         if constexpr (sizeof(T) == 2) {
-          const float lo[4] = {bf16_lo(v[i].x), bf16_hi(v[i].x), bf16_lo(v[i].y), bf16_hi(v[i].y)};
-          const float hi[4] = {bf16_lo(v[i].z), bf16_hi(v[i].z), bf16_lo(v[i].w), bf16_hi(v[i].w)};
-          *reinterpret_cast<uint2*>(qr + static_cast<int64_t>(at) * 8) =
-              make_uint2(quant_pack4(lo, s, inv), quant_pack4(hi, s, inv));
+          *reinterpret_cast<uint2*>(qr + static_cast<int64_t>(at) * 8) = quant_pack8(v[i], s, inv);
         } else {
           const float f[4] = {__uint_as_float(v[i].x), __uint_as_float(v[i].y), __uint_as_float(v[i].z),
                               __uint_as_float(v[i].w)};
@@ -184,12 +194,18 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quantize_rows_warp_kernel(co
   }
 }
 
+// The fewest warps that hold a row of vecs vectors, more while the SMs have few.
+static int quant_warps(int64_t n_rows, int vecs) {
+  int w = 1;
+  while (w < 8 && (vecs > 32 * kQuantVecs * w || n_rows * w < kQuantWarps * num_sms())) w *= 2;
+  return w;
+}
+
 template <typename T>
 static cudaError_t run_quantize_rows(const T* x, int64_t n_rows, int n_cols, int8_t* q, float* scale,
                                      cudaStream_t st) {
   const int vecs = n_cols / (16 / static_cast<int>(sizeof(T)));
-  int w = 1;
-  while (w < 8 && (vecs > 32 * kQuantVecs * w || n_rows * w < kQuantWarps * num_sms())) w *= 2;
+  const int w = quant_warps(n_rows, vecs);
   if (vecs <= 32 * kQuantVecs * w) {
     const int teams = kQuantThreads / 32 / w;
     const int64_t blocks = (n_rows + teams - 1) / teams;
@@ -213,8 +229,54 @@ cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t n_rows, int n
   return run_quantize_rows(static_cast<const float*>(x), n_rows, n_cols, q, scale, st);
 }
 
-// One block per token: the row is read once, its 8 bits go to every kept pair's
-// row (a token is stored up to K + 1 times, read once).
+// Tokens to the rows of their kept pairs: a token is read once and stored up to
+// K + 1 times.  W warps per token, as for rows
+// (16384 tokens of 2048, top-4: 39 -> 22 us against a block that reads each twice).
+template <int W>
+__global__ void __launch_bounds__(kQuantThreads, 4) quantize_dispatch_warp_kernel(
+    const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ slot_of, int64_t T, int d, int K,
+    int64_t max_rows, int8_t* __restrict__ x_q, float* __restrict__ x_scale, unsigned* __restrict__ amax,
+    int8_t* __restrict__ xs_q, float* __restrict__ xs_scale, unsigned* __restrict__ amax_s) {
+  constexpr int kTeams = kQuantThreads / 32 / W;
+  __shared__ unsigned s_max[2][kQuantThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int team = (threadIdx.x >> 5) / W, vecs = d / 8;
+  const int lane = threadIdx.x - team * W * 32;
+  int turn = 0;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + team; t < T;
+       t += static_cast<int64_t>(gridDim.x) * kTeams, turn ^= 1) {
+    int mine = -1;  // lane k of every warp: the slot of choice k
+    if ((lane & 31) < K) mine = slot_of[t * K + (lane & 31)];
+    if (mine >= max_rows) mine = -1;
+    uint4 v[kQuantVecs];
+    const float s = quant_scale(load_row<__nv_bfloat16, W>(x + t * d, vecs, lane, team, s_max, turn, v));
+    const float inv = 1.0f / s;
+    uint2 p[kQuantVecs];
+#pragma unroll
+    for (int i = 0; i < kQuantVecs; ++i) p[i] = quant_pack8(v[i], s, inv);
+    for (int k = xs_q ? -1 : 0; k < K; ++k) {
+      const int slot = __shfl_sync(0xffffffffu, mine, k < 0 ? 0 : k);
+      if (k >= 0 && slot < 0) continue;
+      int8_t* out = k < 0 ? xs_q + t * d : x_q + static_cast<int64_t>(slot) * d;
+#pragma unroll
+      for (int i = 0; i < kQuantVecs; ++i) {
+        const int at = lane + i * 32 * W;
+        if (at < vecs) *reinterpret_cast<uint2*>(out + static_cast<int64_t>(at) * 8) = p[i];
+      }
+    }
+    if (lane < 32 && mine >= 0) {
+      x_scale[mine] = s;
+      amax[mine] = 0;
+    }
+    if (lane == 0 && xs_q) {
+      xs_scale[t] = s;
+      amax_s[t] = 0;
+    }
+  }
+}
+
+// Rows of more than 16384 values: one block per token, which reads it twice.
 __global__ void __launch_bounds__(kQuantThreads) quantize_dispatch_kernel(
     const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ slot_of, int64_t T, int d, int K,
     int64_t max_rows, int8_t* __restrict__ x_q, float* __restrict__ x_scale, unsigned* __restrict__ amax,
@@ -262,6 +324,20 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_dispatch_kernel(
 cudaError_t launch_quantize_dispatch(const Problem& p, const void* x, const int32_t* slot_of, int8_t* x_q,
                                      float* x_scale, unsigned* amax, int8_t* xs_q, float* xs_scale, unsigned* amax_s,
                                      cudaStream_t st) {
+  const int vecs = p.d / 8, w = quant_warps(p.T, vecs);
+  if (vecs <= 32 * kQuantVecs * w) {
+    const int teams = kQuantThreads / 32 / w;
+    const int64_t blocks = (p.T + teams - 1) / teams;
+    const auto run = [&](auto kernel) {
+      return launch_k(kernel, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)), dim3(kQuantThreads), 0, st,
+                      static_cast<const __nv_bfloat16*>(x), slot_of, p.T, p.d, p.K, p.max_rows, x_q, x_scale, amax,
+                      xs_q, xs_scale, amax_s);
+    };
+    if (w == 1) return run(quantize_dispatch_warp_kernel<1>);
+    if (w == 2) return run(quantize_dispatch_warp_kernel<2>);
+    if (w == 4) return run(quantize_dispatch_warp_kernel<4>);
+    return run(quantize_dispatch_warp_kernel<8>);
+  }
   const unsigned grid = static_cast<unsigned>(p.T < 65536 ? p.T : 65536);
   return launch_k(quantize_dispatch_kernel, dim3(grid), dim3(kQuantThreads), 0, st,
                   static_cast<const __nv_bfloat16*>(x), slot_of, p.T, p.d, p.K, p.max_rows, x_q, x_scale, amax, xs_q,

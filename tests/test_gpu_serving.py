@@ -83,6 +83,25 @@ def test_layer_forward_i8(T, d, E, K, F, Ns, C):
         assert torch.allclose(layer.stats, stats, rtol=4e-7, atol=0)
 
 
+@pytest.mark.parametrize("T,d,Ns,C", [(1250, 2064, 1, 0.5), (200, 4112, 0, 0.0), (90, 8208, 1, 1.0), (70, 16400, 1, 0.7)])
+def test_wide_tokens_reach_their_rows(T, d, Ns, C):
+    """Tokens that take several warps, or a whole block twice, to round; dropped pairs."""
+    inp = inputs(T, 64, 4, 2, 48, Ns, T + d)  # exact logits of 64 values; the rest has no say in the routing
+    g = torch.Generator().manual_seed(d)
+    for k in [k for k in ("x", "w_gate", "w13", "w13_shared") if k in inp]:
+        more = torch.zeros if k == "w_gate" else (lambda s: torch.randn(s, generator=g) * (1 if k == "x" else d ** -0.5))
+        t = torch.as_tensor(inp[k])
+        inp[k] = torch.cat([t, more((*t.shape[:-1], d - 64)).to(t.dtype)], -1)
+    for k in [k for k in ("w2", "w2_shared") if k in inp]:
+        inp[k] = (torch.randn((*inp[k].shape[:-2], d, 48), generator=g) / 48 ** 0.5).to(torch.bfloat16)
+    layer = MoeLayerI8.from_layer(layer_of(inp, 2, 48, Ns, C))
+    y = layer.forward(inp["x"].cuda())
+    assert api.read_device_status(layer.ws) == 0
+    want = ref.few_layer(quantised(inp), 2, [api.capacity(layer.prob)] * 4, False)
+    assert torch.equal(layer.routing["slot_of"].cpu(), want["slot_of"].reshape(T, 2))
+    check(y, want, True)
+
+
 @pytest.mark.parametrize("cls", [MoeLayer, MoeLayerI8])
 def test_the_forwards_of_one_layer_agree(cls):
     """forward, forward_few, a captured forward and forward_host of the same
