@@ -31,17 +31,19 @@
 // multiplied in some 500), which is why the simple warp-level instruction is
 // used and not tcgen05: its 128-row tiles would be 1..8 rows full.  FP32
 // weights take fused multiply-adds (8 rows x 8 tokens per lane).  Sums are FP32
-// or int32; BF16 layers round the hidden rows to BF16, as moe_layer_forward
-// does (they are the tensor cores' operand), and nothing else before y.  No
-// step depends on the order in which CTAs run, so results repeat bit for bit.
+// or int32; BF16 layers keep a hidden value as the sum of two BF16 (the tensor
+// cores' operands, 16 bits in all) and round nothing else before y.  No step
+// depends on the order in which CTAs run, so results repeat bit for bit.
 //
 // What bounds it: the weights' stream.  us per call, and of the measured copy
 // bandwidth (6540 GB/s) that the weights alone make up: 32 tokens, d = 4096,
-// E = 128, F = 1536, top-8 + 1 shared 640 (1.0); one token, d = 4096, E = 8,
-// F = 14336, top-2 127 (0.85); one token, d = 2048, E = 128, F = 1024, top-8 + 4
-// shared 51 (0.45).  The last is where the rest shows: 12 us until the experts are
-// known (logits 3, barrier 2, top-K 5, slots 2), three more grid barriers of 1.7
-// us, 3 us for the combine, 4 us between two launches.
+// E = 128, F = 1536, top-8 + 1 shared 654 (0.99); one token, d = 4096, E = 8,
+// F = 14336, top-2 125 (0.86); one token, d = 2048, E = 128, F = 1024, top-8 + 4
+// shared 45 (0.51).  The last is where the rest shows: 8.5 us until the experts are
+// known (logits 3, barrier 2, top-K 2, slots 1), three more grid barriers of 2 us,
+// 3 us for the combine, 2 us between two launches.  Code that runs once per call is
+// fetched from memory first, so it is short and has one copy: a second inlined call
+// of the selection alone cost 3 us.
 //
 // Every wait is bounded (mbar_wait, few_grid_sync); after a time-out the kernel
 // issues no more copies, waits for those in flight and reports
@@ -235,6 +237,9 @@ struct Few : FewTile<WT> {
   // warps' sums and stores them, the other multiplies.
   static constexpr int kTeams = WT == kFewF32 ? 1 : 2;
   static constexpr int kTeamWarps = kFewWorkers / 32 / kTeams;
+  // BF16: a hidden value is the sum of two BF16, 16 bits in all, each a row of its
+  // own in the token buffer (see few_store_unit).
+  static constexpr int kParts = kW == 2 ? 2 : 1;
   using Acc = typename std::conditional<WT == kFewI8, int, float>::type;
 
   const FewArgs& a;
@@ -248,6 +253,9 @@ struct Few : FewTile<WT> {
       : a(a_), s(s_), ring(ring_), tok(tok_), cta(blockIdx.x), n_cta(gridDim.x), nfb(a_.F / 8),
         nb((a_.d + kFewRows - 1) / kFewRows), sg_up((a_.T + a_.ng_up - 1) / a_.ng_up),
         sg_down((a_.T + a_.ng_down - 1) / a_.ng_down) {}
+
+  // rows of the hidden buffer in front of the low parts
+  __device__ __forceinline__ int64_t low_rows(bool routed) const { return static_cast<int64_t>(a.T) * (routed ? a.K : a.Ns); }
 
   // units of a pass (fewer than 2^31: few_supported)
   __device__ __forceinline__ unsigned units(int pass) const {
@@ -427,6 +435,7 @@ template <int WT>
 struct FewMathMma {
   using Acc = typename Few<WT>::Acc;
   static constexpr int kWarps = Few<WT>::kTeamWarps, kChunk = FewTile<WT>::kChunk, kPitch = FewTile<WT>::kPitch;
+  static constexpr int kParts = Few<WT>::kParts;
   // [token tile][chain]: two chains of dependent products instead of one twice
   // as long
   Acc acc[2][2][4];
@@ -436,35 +445,29 @@ struct FewMathMma {
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[j >> 1][j & 1][i] = 0;
   }
-  // w: the stage; t: the token buffer at the stage's first byte of the rows
-  __device__ __forceinline__ void stage(const uint8_t* w, const uint8_t* t, int t_pitch, int cb, int n_tok, int rows,
-                                        int warp, int lane) {
+  // w: the stage; t: the token buffer at the stage's first byte of the rows; low:
+  // distance to the rows that are added to them, or 0
+  __device__ __forceinline__ void stage(const uint8_t* w, const uint8_t* t, int t_pitch, int low, int cb, int n_tok,
+                                        int rows, int warp, int lane) {
     // ldmatrix lane addresses: weights as four 8 x 16-byte blocks (rows 0-7 and
     // 8-15, bytes 0-15 and 16-31); tokens as 8 rows x 64 bytes
     const uint32_t wa = smem_addr(w) + (lane & 15) * kPitch + (lane >> 4) * 16;
     // (rows past the group's last repeat it: their sums are not read)
     const uint32_t ta = smem_addr(t) + min(lane & 7, n_tok - 1) * t_pitch + (lane >> 3) * 16;
     const uint32_t tb = smem_addr(t) + min(8 + (lane & 7), n_tok - 1) * t_pitch + (lane >> 3) * 16;
-    if (cb == kChunk && rows == kFewRows) {  // whole stage
+    if (cb == kChunk && rows == kFewRows) {
 #pragma unroll
       for (int i = 0; i < kChunk / (64 * kWarps); ++i) {
         const int o = (i * kWarps + warp) * 64;
-        uint32_t a0[4], a1[4], b[4];
+        uint32_t a0[4], a1[4];
         ldmatrix_x4(wa + o, a0);
         ldmatrix_x4(wa + o + 32, a1);
-        ldmatrix_x4(ta + o, b);
-        mma_16x8(acc[0][0], a0, b[0], b[1]);
-        mma_16x8(acc[0][1], a1, b[2], b[3]);
-        if (n_tok > 8) {
-          ldmatrix_x4(tb + o, b);
-          mma_16x8(acc[1][0], a0, b[0], b[1]);
-          mma_16x8(acc[1][1], a1, b[2], b[3]);
-        }
+        tokens(ta + o, tb + o, low, n_tok, a0, a1);
       }
       return;
     }
     for (int o = warp * 64; o < cb; o += kWarps * 64) {
-      uint32_t a0[4], a1[4], b[4];
+      uint32_t a0[4], a1[4];
       ldmatrix_x4(wa + o, a0);
       ldmatrix_x4(wa + o + 32, a1);
       if (o + 64 > cb) {  // the row ends inside: what lies behind it may be anything
@@ -473,11 +476,27 @@ struct FewMathMma {
         if (o + 48 >= cb) a1[2] = a1[3] = 0;
       }
       if (rows == 8) a0[1] = a0[3] = a1[1] = a1[3] = 0;
-      ldmatrix_x4(ta + o, b);
+      tokens(ta + o, tb + o, low, n_tok, a0, a1);
+    }
+  }
+  // 64 bytes of the tokens' rows with the weights a0 (bytes 0-31), a1 (32-63)
+  __device__ __forceinline__ void tokens(uint32_t ta, uint32_t tb, int low, int n_tok, const uint32_t (&a0)[4],
+                                         const uint32_t (&a1)[4]) {
+    uint32_t b[4];
+    ldmatrix_x4(ta, b);
+    mma_16x8(acc[0][0], a0, b[0], b[1]);
+    mma_16x8(acc[0][1], a1, b[2], b[3]);
+    if (kParts > 1 && low) {
+      ldmatrix_x4(ta + low, b);
       mma_16x8(acc[0][0], a0, b[0], b[1]);
       mma_16x8(acc[0][1], a1, b[2], b[3]);
-      if (n_tok > 8) {
-        ldmatrix_x4(tb + o, b);
+    }
+    if (n_tok > 8) {
+      ldmatrix_x4(tb, b);
+      mma_16x8(acc[1][0], a0, b[0], b[1]);
+      mma_16x8(acc[1][1], a1, b[2], b[3]);
+      if (kParts > 1 && low) {
+        ldmatrix_x4(tb + low, b);
         mma_16x8(acc[1][0], a0, b[0], b[1]);
         mma_16x8(acc[1][1], a1, b[2], b[3]);
       }
@@ -523,7 +542,7 @@ struct FewMath<kFewF32> {
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[r][j] = 0.f;
   }
-  __device__ __forceinline__ void stage(const uint8_t* w, const uint8_t* t, int t_pitch, int cb, int n_tok, int rows,
+  __device__ __forceinline__ void stage(const uint8_t* w, const uint8_t* t, int t_pitch, int, int cb, int n_tok, int rows,
                                         int warp, int lane) {
     const int o = (warp & 3) * 512 + lane * 16;
     if (o >= cb || (warp >> 2) * 8 >= rows) return;
@@ -600,19 +619,24 @@ __device__ __forceinline__ void few_load_tokens(const Few<WT>& f, int pass, cons
   const bool up = pass <= kUpRouted;
   const bool routed = pass == kUpRouted || pass == kDownRouted;
   const int vecs = q.len / 16, all = ((q.len + 63) & ~63) / 16;
-  // 256 / (n rounded up to a power of two) threads per row
-  const int sh = __clz(q.n - 1) - 24;
+  const int n_rows = up ? q.n : q.n * Few<WT>::kParts;  // hidden rows: the high parts, then the low ones
+  // 256 / (rows rounded up to a power of two) threads per row
+  const int sh = __clz(n_rows - 1) - 24;
   const int per = 1 << sh, r = tid >> sh, v0 = tid & (per - 1);
   if (WT != kFewI8 || up) {
-    if (r < q.n) {
+    if (r < n_rows) {
       const char* src;
-      if (up)
+      if (up) {
         src = static_cast<const char*>(WT == kFewI8 ? static_cast<const void*>(a.x_q) : a.x) +
               static_cast<int64_t>(routed ? f.s.perm[q.row0 + r] / a.K : q.row0 + r) * q.len;
-      else
-        src = static_cast<const char*>(routed ? a.h : a.h_s) +
-              (routed ? q.row0 + r : static_cast<int64_t>(q.row0 + r) * a.Ns + q.e) * a.F * Few<WT>::kW +
+      } else {
+        const bool low = r >= q.n;
+        int64_t row = q.row0 + (low ? r - q.n : r);
+        if (!routed) row = row * a.Ns + q.e;
+        if (low) row += f.low_rows(routed);
+        src = static_cast<const char*>(routed ? a.h : a.h_s) + row * a.F * Few<WT>::kW +
               static_cast<int64_t>(q.c) * a.chunk_bytes;
+      }
       const uint32_t dst = smem_addr(tok + r * t_pitch);
       for (int v = v0; v < all; v += per) {
         const bool in = v < vecs;
@@ -726,10 +750,18 @@ __device__ __forceinline__ void few_store_unit(const Few<WT>& f, int pass, const
       const int64_t row = q.row0 + tok;
       const int64_t at = pass == kUpShared ? (row * a.Ns + q.e) * a.F + q.col + ft : row * a.F + q.col + ft;
       void* hp = pass == kUpShared ? a.h_s : a.h;
-      if constexpr (Few<WT>::kW == 2)
-        static_cast<__nv_bfloat16*>(hp)[at] = __float2bfloat16(h);
-      else
+      if constexpr (Few<WT>::kParts == 2) {
+        // h = high + low, off by at most 2^-16 of it: one BF16, the tensor cores'
+        // operand, would put as much rounding into y as y's own (32 tokens,
+        // d = 4096, E = 128 638 -> 654 us; one token, d = 2048 43.5 -> 45.4 us).  Infinities and NaN stay in the high part.
+        const __nv_bfloat16 high = __float2bfloat16(h);
+        const float rest = h - __bfloat162float(high);
+        static_cast<__nv_bfloat16*>(hp)[at] = high;
+        static_cast<__nv_bfloat16*>(hp)[at + f.low_rows(pass == kUpRouted) * a.F] =
+            __float2bfloat16(isfinite(rest) ? rest : 0.f);
+      } else {
         static_cast<float*>(hp)[at] = h;
+      }
     }
     if constexpr (WT == kFewI8) {
       unsigned m = abs_bits(h);
@@ -767,6 +799,7 @@ __device__ __forceinline__ void few_passes(const Few<WT>& f, int first_pass, uin
   const int lane = tid & 31, team = (tid >> 5) / kWarps, warp = (tid >> 5) % kWarps;
   FewMath<WT> math;
   red_base += team * (kFewRedBytes / kTeams);
+  const int parts = first_pass == kDownShared ? Few<WT>::kParts : 1;  // rows of a token in its buffer
   Place<WT> here(f, first_pass);
   int loaded = 0;           // spans, from this one on, whose rows are in the token buffer,
   int at = 0, row = 0;      // the next one's at byte `at`, their scales at `row`
@@ -788,13 +821,13 @@ __device__ __forceinline__ void few_passes(const Few<WT>& f, int first_pass, uin
         Span n = q;
         int bytes = 0, rows = 0;
         for (;;) {
-          const int pitch = few_token_pitch(n.len);
-          few_load_tokens(f, p.pass, n, f.tok + bytes, f.s.row_scale + rows, pitch, tid);
+          const int pitch = few_token_pitch(n.len) * parts;
+          few_load_tokens(f, p.pass, n, f.tok + bytes, f.s.row_scale + rows, few_token_pitch(n.len), tid);
           bytes += n.n * pitch;
           rows += n.n;
           if (key >= 0 || !p.more(f)) break;
           n = f.span(p.pass, p.u, p.last);
-          if (rows + n.n > 16 || bytes + n.n * few_token_pitch(n.len) > Few<WT>::kTokBytes) break;
+          if (rows + n.n > 16 || bytes + n.n * few_token_pitch(n.len) * parts > Few<WT>::kTokBytes) break;
           p.u += n.units;
           ++loaded;
         }
@@ -806,7 +839,8 @@ __device__ __forceinline__ void few_passes(const Few<WT>& f, int first_pass, uin
     --loaded;
     const uint8_t* tok = f.tok + at;
     const float* row_scale = f.s.row_scale + row;
-    at += q.n * t_pitch;
+    at += q.n * t_pitch * parts;
+    const int low = parts > 1 ? q.n * t_pitch : 0;
     row += q.n;
     q.col += team * q.step;
     // 8-bit weights: the scales are fetched one unit ahead (fetched when needed
@@ -824,7 +858,7 @@ __device__ __forceinline__ void few_passes(const Few<WT>& f, int first_pass, uin
         const int slot = team * kSlots + static_cast<int>(used % kSlots);
         mbar_wait(&f.s.full[slot], (used / kSlots) & 1u, &f.s.abort_flag);
         __syncwarp();
-        math.stage(f.ring + slot * Few<WT>::kStageBytes, tok + off, t_pitch, min(kChunk, q.len - off), q.n, rows,
+        math.stage(f.ring + slot * Few<WT>::kStageBytes, tok + off, t_pitch, low, min(kChunk, q.len - off), q.n, rows,
                    warp, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&f.s.empty[slot]);
@@ -1221,14 +1255,15 @@ bool few_supported(const Problem& p, bool i8) {
 static void few_tiling(const Problem& p, bool i8, int tok_bytes, FewArgs* a) {
   const int64_t ws = static_cast<int64_t>(few_weight_bytes(p, i8));
   const int64_t most = p.dtype == kF32 && !i8 ? 8 : 16;
-  auto rows = [&](int64_t bytes) {
-    const int64_t n = tok_bytes / few_pitch(bytes);
+  auto rows = [&](int64_t bytes, int parts) {
+    const int64_t n = tok_bytes / (few_pitch(bytes) * parts);
     return static_cast<int>(n < most ? n : most);
   };
-  a->ng_up = rows(p.d * ws);
+  const int parts = p.dtype == kBF16 && !i8 ? 2 : 1;  // of a hidden value
+  a->ng_up = rows(p.d * ws, 1);
   const int64_t fb = p.F * ws;
-  const int64_t want = p.T < 8 ? p.T : 8;
-  int64_t longest = (tok_bytes / want - 80) / 2048 * 2048;
+  const int64_t want = (p.T < 8 ? p.T : 8) * parts;
+  int64_t longest = (FewTile<kFewBF16>::kTokBytes / want - 80) / 2048 * 2048;
   // 8 KB give every CTA many units: with one chunk of 28 KB (F = 14336, one
   // token) a CTA had 3 or 4 units and the down product ended 15% late
   if (longest > 8192) longest = 8192;
@@ -1237,7 +1272,7 @@ static void few_tiling(const Problem& p, bool i8, int tok_bytes, FewArgs* a) {
   const int64_t chunk = (even + 63) / 64 * 64;  // chunks of equal length: units of equal cost
   a->nc = static_cast<int>((fb + chunk - 1) / chunk);
   a->chunk_bytes = static_cast<int>(chunk);
-  a->ng_down = rows(fb < chunk ? fb : chunk);
+  a->ng_down = rows(fb < chunk ? fb : chunk, parts);
 }
 
 // Reads of the experts' weights, about: an expert whose rows do not fit one
@@ -1375,7 +1410,7 @@ cudaError_t launch_few_layer(const Problem& p, const FewCall& c, cudaStream_t st
   if (!c.i8 && p.dtype == kBF16) {
     FewArgs m = a;
     few_tiling(p, false, FewTile<kFewBF16Many>::kTokBytes, &m);
-    if (m.nc == a.nc && few_reads(p, m) < 0.9 * few_reads(p, a)) {
+    if (few_reads(p, m) < 0.9 * few_reads(p, a)) {
       a = m;
       many = true;
     }

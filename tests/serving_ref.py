@@ -86,9 +86,10 @@ def dispatch(idx, E, caps):
             torch.tensor(off, dtype=torch.int32), torch.tensor(slot, dtype=torch.int32))
 
 
-def expert(x, w13, w2, bf16: bool):
+def expert(x, w13, w2, bf16):
     """One SwiGLU expert on float64 rows and the bound on the library's form:
-    32-bit sums, the hidden row rounded to BF16 (bf16) or kept in FP32."""
+    32-bit sums, the hidden row kept in FP32 (False), rounded to BF16 (True), or
+    kept as a sum of two BF16 ("pair")."""
     F, d = w13.shape[0] // 2, w13.shape[1]
     w13, w2 = w13.double(), w2.double()
     z, za = x @ w13.T, (x.abs() @ w13.abs().T) * ((d + 2) * U)
@@ -97,13 +98,14 @@ def expert(x, w13, w2, bf16: bool):
     # |d silu / dg| <= 1.1; the error of g times |u|, of u times |silu(g)|
     eh = 1.1 * za[:, :F] * (u.abs() + za[:, F:]) + (g * torch.sigmoid(g)).abs() * za[:, F:] + SILU * h.abs()
     if bf16:
-        eh = eh + BF16_HALF * (h.abs() + eh)
+        # a pair: the rest, at most 2^-8 of h, is off by 2^-8 of itself; the product with each part sums F terms
+        eh = eh + BF16_HALF ** (2 if bf16 == "pair" else 1) * (h.abs() + eh)
     y = h @ w2.T
-    ey = eh @ w2.abs().T + ((h.abs() + eh) @ w2.abs().T) * ((F + 8) * U)
+    ey = eh @ w2.abs().T + ((h.abs() + eh) @ w2.abs().T) * ((F + 8) * U * (2 if bf16 == "pair" else 1))
     return y, ey
 
 
-def few_layer(inp: dict, K: int, caps, bf16: bool, bias_on_logit=False, logits=None):
+def few_layer(inp: dict, K: int, caps, bf16, bias_on_logit=False, logits=None):
     """The layer from CPU inputs: dict of routing, y and its bound (before the
     rounding to the activations' type), and mag, the magnitudes of the expert
     outputs that make up y (times their gates): a form that rounds them to BF16

@@ -83,7 +83,7 @@ def run(T, d, E, K, F, Ns=0, kind="bf16", C=0.0, flags=0, caps=None, seed=0, bia
     layer = build(inp, K, C, flags, caps, Ns)
     x = inp["x"].cuda()
     y = layer.forward_few(x)
-    want = ref.few_layer(inp, K, caps if caps is not None else limits(T, E, K, C), kind == "bf16",
+    want = ref.few_layer(inp, K, caps if caps is not None else limits(T, E, K, C), kind == "bf16" and "pair",
                          bool(flags & api.FLAG_BIAS_LOGIT))
     # |w error| <= (K + 16) u on each expert's output: bounded by the sum of their magnitudes
     want["gate_slack"] = (K + 16) * ref.U * K * want["y"].abs().amax() * torch.ones_like(want["y"])
@@ -147,7 +147,7 @@ def test_few_layer_given_logits(kind):
     logits[5, 1:] = -3e38
     layer.routing["logits"].copy_(logits)
     y = layer.forward_few(inp["x"].cuda())
-    want = ref.few_layer(inp, K, [-1] * E, kind == "bf16", logits=logits.double())
+    want = ref.few_layer(inp, K, [-1] * E, kind == "bf16" and "pair", logits=logits.double())
     want["gate_slack"] = (K + 16) * ref.U * K * want["y"].abs().amax() * torch.ones_like(want["y"])
     check(layer, y, want, inp["x"].dtype)
 
