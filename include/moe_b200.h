@@ -396,8 +396,9 @@ int moe_layer_backward(const moe_problem_t* p, const void* x, const moe_weights_
  *   - ws: moe_few_workspace_size bytes, 256-byte aligned; any contents.  The
  *     status word is its first word, as everywhere, and is reset by the call;
  *   - logits are summed in FP32 and FP64, expert outputs stay in FP32 up to
- *     the combine (moe_layer_forward rounds them to the activations' type
- *     first), so the two entry points agree to rounding, not bit for bit.
+ *     the combine and hidden activations keep 16 bits or more
+ *     (moe_layer_forward rounds both to the activations' type), so the two
+ *     entry points agree to rounding, not bit for bit.
  *     Results of one entry point repeat bit for bit;
  *   - MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_TOKENS, or a d_model whose row
  *     of weights exceeds 69568 bytes (34784 for BF16, 17392 for FP32, 69568

@@ -1405,7 +1405,8 @@ cudaError_t launch_few_layer(const Problem& p, const FewCall& c, cudaStream_t st
   few_tiling(p, c.i8, FewTile<kFewBF16>::kTokBytes, &a);
   // BF16 rows of more than 4 KB: 16 rows fit the token buffer only with half the
   // ring.  Taken when that saves a tenth of the reads (d = 4096, E = 8,
-  // F = 14336, top-2: 48 tokens 825 -> 580 us, 64 tokens 1024 -> 755 us).
+  // F = 14336, top-2: 48 tokens 825 -> 580 us, 64 tokens 1024 -> 755 us; measured
+  // before the hidden rows got their low parts).
   bool many = false;
   if (!c.i8 && p.dtype == kBF16) {
     FewArgs m = a;
