@@ -45,11 +45,14 @@
 // fetched from memory first, so it is short and has one copy: a second inlined call
 // of the selection alone cost 3 us.
 //
-// Every wait is bounded (mbar_wait, few_grid_sync); after a time-out the kernel
-// issues no more copies, waits for those in flight and reports
-// MOE_DEV_WAIT_TIMEOUT.  The first grid barrier is cooperative groups' own,
-// which needs no cleared memory, and clears the counters of the others.  All
-// CTAs are resident (cooperative launch) and each reaches every barrier.
+// The first grid barrier is cooperative groups' own, which needs no cleared
+// memory; it has no time limit and needs none: all CTAs are resident (cooperative
+// launch) and none waits for anything before it.  CTA 0 clears the counters of
+// the others in front of it.  Every wait behind it is bounded (mbar_wait,
+// few_grid_sync).  A CTA in which one runs out issues no more copies, runs no
+// further pass and no combine (what other CTAs were to write may be missing, row
+// indices among it), still arrives at every barrier, waits for its copies in
+// flight and reports MOE_DEV_WAIT_TIMEOUT.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -87,7 +90,9 @@ struct FewShared {
   int groups[2][kMaxExperts + 1];         // prefix of the experts' token groups: up, down
   uint16_t perm[kFewMaxPairs];            // slot -> t * K + k
   float row_scale[16];                    // 8-bit tokens: scale of each row in the token buffer
-  int abort_flag;
+  uint64_t never;                         // a barrier that nothing arrives on (test_stall)
+  int abort_flag;                         // raised by whoever gave up a wait
+  int gave_up;                            // the worker threads' common view of it (few_grid_sync)
 };
 
 constexpr int few_smem_bytes() {
@@ -148,6 +153,7 @@ struct FewArgs {
   float alpha;
   double pscale;
   int spread;          // top-K: one token per CTA instead of every CTA all tokens
+  unsigned long long stall_ns;  // abort-path test hook (test_stall), 0 normally
   // tiling (host): token rows per group, reduction chunks of the down product
   int ng_up, ng_down, nc, chunk_bytes;
 };
@@ -186,24 +192,29 @@ __device__ __forceinline__ void mma_16x8(int (&c)[4], const uint32_t (&a)[4], ui
 // Grid barrier of the worker threads: the CTA's writes before it are seen by
 // every CTA's reads (past L1) after it.  All CTAs are resident and every one
 // of them arrives whatever its copies do; the wait is bounded all the same.
-__device__ __forceinline__ void few_grid_sync(unsigned* arrivals, int* abort_flag, int tid) {
+// Whether the CTA may go on: false once any wait in it was given up, the same in
+// all worker threads (thread 0 decides; a copying warp may raise the flag any time).
+__device__ __forceinline__ bool few_grid_sync(unsigned* arrivals, FewShared& s, unsigned long long limit_ns, int tid) {
   named_bar_sync(1, kFewWorkers);
   if (tid == 0) {
     __threadfence();
     atomicAdd(arrivals, 1u);
     const unsigned long long t0 = global_ns();
+    volatile int* abort_flag = &s.abort_flag;
     unsigned n;
     for (unsigned i = 1;; ++i) {
       asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(n) : "l"(arrivals) : "memory");
       if (n >= gridDim.x) break;
-      if ((i & 255u) == 0 && global_ns() - t0 > kWaitLimitNs) {
-        *reinterpret_cast<volatile int*>(abort_flag) = 1;
+      if ((i & 255u) == 0 && (*abort_flag || global_ns() - t0 > limit_ns)) {
+        *abort_flag = 1;
         break;
       }
     }
     __threadfence();
+    s.gave_up = *abort_flag;
   }
   named_bar_sync(1, kFewWorkers);
+  return s.gave_up == 0;
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
@@ -1135,6 +1146,7 @@ __global__ void __launch_bounds__(FewTile<WT>::kThreads, 1) few_layer_kernel(con
       mbar_init(&s.full[i], kCopiers);
       mbar_init(&s.empty[i], Few<WT>::kTeamWarps);
     }
+    mbar_init(&s.never, 1);
     s.abort_flag = 0;
     fence_barrier_init();
   }
@@ -1168,6 +1180,10 @@ __global__ void __launch_bounds__(FewTile<WT>::kThreads, 1) few_layer_kernel(con
   }
   grid.sync();
 
+  bool go = true;  // false: a wait was given up (workers; the same in all of them)
+  // the tests' stalled run: CTA 0 comes late, the other CTAs wait a quarter of that
+  const unsigned long long limit_ns = a.stall_ns ? a.stall_ns / 4 : kWaitLimitNs;
+  if (a.stall_ns && blockIdx.x == 0 && tid == 0) test_stall(&s.never, &s.abort_flag, a.stall_ns);
   if (worker) {
     int32_t* idx = reinterpret_cast<int32_t*>(tok);
     const bool write = blockIdx.x == 0;
@@ -1177,7 +1193,9 @@ __global__ void __launch_bounds__(FewTile<WT>::kThreads, 1) few_layer_kernel(con
                    a.spread ? blockIdx.x + warp * gridDim.x : warp, (a.spread ? gridDim.x : 1) * (kFewWorkers / 32),
                    lane);
     if (a.spread) {
-      few_grid_sync(a.arrivals, &s.abort_flag, tid);
+      // (given up: some entries may be missing; few_dispatch takes any values, and
+      // the copying warps need the counts that it makes)
+      go = few_grid_sync(a.arrivals, s, limit_ns, tid);
 #pragma unroll 1
       for (int i = tid; i < a.T * a.K; i += kFewWorkers) idx[i] = __ldcg(a.topk_idx + i);
     }
@@ -1190,8 +1208,8 @@ __global__ void __launch_bounds__(FewTile<WT>::kThreads, 1) few_layer_kernel(con
     // fetched from memory first (the weights' stream evicts it between calls)
 #pragma unroll 1
     for (int pass = kUpShared; pass <= kDownShared; pass += kDownShared - kUpShared) {
-      if (pass == kDownShared) few_grid_sync(a.arrivals + 1, &s.abort_flag, tid);
-      few_passes(f, pass, used, red, n_units, held, tid);
+      if (pass == kDownShared) go = few_grid_sync(a.arrivals + 1, s, limit_ns, tid);
+      if (go) few_passes(f, pass, used, red, n_units, held, tid);
     }
     // the gates and slots of the combine, while the other CTAs finish
     named_bar_sync(1, kFewWorkers);
@@ -1199,23 +1217,16 @@ __global__ void __launch_bounds__(FewTile<WT>::kThreads, 1) few_layer_kernel(con
     float* gate = reinterpret_cast<float*>(tok) + kFewMaxPairs;
 #pragma unroll 1
     for (int i = tid; i < a.T * a.K; i += kFewWorkers) {
-      slot[i] = __ldcg(a.slot_of + i);
+      // (CTA 0 wrote them before the barrier behind the up pass; no value, not
+      // even one that it had no time to write, is used as a row that is not there)
+      const int sl = __ldcg(a.slot_of + i);
+      slot[i] = static_cast<unsigned>(sl) < static_cast<unsigned>(s.seg_off[a.E]) ? sl : -1;
       gate[i] = __ldcg(a.topk_w + i);
     }
-    few_grid_sync(a.arrivals + 2, &s.abort_flag, tid);
-    few_combine<X>(a, slot, gate, tid);
+    go = few_grid_sync(a.arrivals + 2, s, limit_ns, tid);
+    if (go) few_combine<X>(a, slot, gate, tid);
   } else if (copies) {
     few_fill(f, cur, kDownRouted, copier, lane);
-    if (lane == 0 && *static_cast<volatile int*>(&s.abort_flag)) {
-      // gave up a wait: let every copy land before the block ends
-      constexpr uint32_t kSlots = kFewStages / Few<WT>::kTeams;
-      int never = 0;
-      for (int t = 0; t < Few<WT>::kTeams; ++t) {
-        const uint32_t n = t ? cur.issued1 : cur.issued0;
-        for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i)
-          mbar_wait(&s.full[t * kSlots + i % kSlots], (i / kSlots) & 1u, &never);
-      }
-    }
   } else if (blockIdx.x == 0 && a.stats) {
     // the statistics, beside the other warps' work
     for (int e = lane; e < a.E; e += 32)
@@ -1231,7 +1242,19 @@ __global__ void __launch_bounds__(FewTile<WT>::kThreads, 1) few_layer_kernel(con
     }
   }
   __syncthreads();
-  if (tid == 0 && *static_cast<volatile int*>(&s.abort_flag)) raise_status(a.status, kDevWaitTimeout);
+  if (*static_cast<volatile int*>(&s.abort_flag)) {
+    if (tid == 0) raise_status(a.status, kDevWaitTimeout);
+    if (copies && lane == 0) {
+      // nobody may have waited for the last copies: let each land before the block ends
+      constexpr uint32_t kSlots = kFewStages / Few<WT>::kTeams;
+      int late = 0;
+      for (int t = 0; t < Few<WT>::kTeams; ++t) {
+        const uint32_t n = t ? cur.issued1 : cur.issued0;
+        for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i)
+          mbar_wait(&s.full[t * kSlots + i % kSlots], (i / kSlots) & 1u, &late);
+      }
+    }
+  }
 }
 
 // ----------------------------------------------------------------- host side
@@ -1402,6 +1425,7 @@ cudaError_t launch_few_layer(const Problem& p, const FewCall& c, cudaStream_t st
   a.extended = (p.flags & 0x4u) ? 1 : 0;
   a.alpha = p.alpha;
   a.pscale = p_fixed_scale(p.T);
+  a.stall_ns = test_stall_ns();
   few_tiling(p, c.i8, FewTile<kFewBF16>::kTokBytes, &a);
   // BF16 rows of more than 4 KB: 16 rows fit the token buffer only with half the
   // ring.  Taken when that saves a tenth of the reads (d = 4096, E = 8,

@@ -261,10 +261,11 @@ int num_sms();
 int cuda_rc(cudaError_t e);
 
 // moe_api.cu: test hook of the bounded-wait abort path.  MOE_B200_TEST_STALL_NS
-// (read at every launch of the fused router and the single-CTA expert GEMM;
-// unset or 0 normally) makes those kernels' MMA thread wait that long for a
-// barrier phase that never completes, so the kernel records
-// MOE_DEV_WAIT_TIMEOUT and returns through its abort path.
+// (read at every launch of the fused router, the single-CTA expert GEMM and the
+// few-token layer; unset or 0 normally) makes those kernels' MMA thread (few-token
+// layer: a thread of CTA 0) wait that long for a barrier phase that never
+// completes, so the kernel records MOE_DEV_WAIT_TIMEOUT and returns through its
+// abort path.
 unsigned long long test_stall_ns();
 
 }  // namespace moe
