@@ -6,6 +6,7 @@ on a non-zero status.  No step of the layer is computed here.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -285,11 +286,25 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+def _stream_handle(stream, dev: int) -> int:
+    return _current_stream(dev) if stream is None else _stream(stream)
+
+
+def _on_stream(stream, dev: int):
+    """Context in which torch allocates and enqueues on `stream` (a torch stream,
+    a handle; None: the current one, nothing changes)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
+    return torch.cuda.stream(stream)
+
+
 def _enqueue(name: str, dev: int, stream, *args) -> None:
     """Call the C entry point `name` with args and the stream handle (`stream`,
     or device dev's current stream), device dev being current."""
     fn = getattr(_lib.lib(), name)
-    st = _current_stream(dev) if stream is None else _stream(stream)
+    st = _stream_handle(stream, dev)
     if torch.cuda.current_device() == dev:
         rc = fn(*args, st)
     else:

@@ -20,7 +20,8 @@ class MoeLayer:
         self.device = torch.device(device)
         self.weights = weights
         self.ws = self._alloc_workspace(prob, self.device)
-        self.few_ws = None  # forward_few's workspace, allocated by its first call
+        self.few_ws = None  # forward_few's workspace, allocated by its first call on that call's stream
+        self._few_stream = None
         self.dtype = torch.bfloat16 if prob.dtype == api.DTYPE_BF16 else torch.float32
         T, E, K = prob.T, prob.n_experts, prob.top_k
         self.routing = None
@@ -78,11 +79,18 @@ class MoeLayer:
         leaves behind.  Its device status is in self.few_ws."""
         if y is None:
             y = torch.empty((self.prob.T, self.prob.d_model), dtype=self.dtype, device=self.device)
+        dev = api._cuda("x", x)
+        handle = api._stream_handle(stream, dev)
         if self.few_ws is None:
             self._check_weights()
-            self.few_ws = api.alloc_few_workspace(self.prob, self.device)
+            with api._on_stream(stream, dev):  # its clearing runs in front of the kernel, on the same stream
+                self.few_ws = api.alloc_few_workspace(self.prob, self.device)
+            self._few_stream = handle
+        elif handle != self._few_stream:  # freed while this stream still uses it, it is not handed out again
+            with api._on_stream(stream, dev):
+                self.few_ws.record_stream(torch.cuda.current_stream(dev))
         self._forward_few(self.prob, x, self.weights, y, self.routing, self.stats if with_stats else None,
-                          self.few_ws, stream)
+                          self.few_ws, handle)
         return y
 
     def _weight_shapes(self) -> dict:

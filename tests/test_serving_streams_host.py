@@ -1,0 +1,87 @@
+"""On which stream the Python layer allocates what it uses on a caller's stream
+(no GPU: torch's stream context and the entry points are stand-ins)."""
+import contextlib
+
+import pytest
+import torch
+
+from sparse_mixture_experts_04_b200 import MoeLayer, api
+
+
+class FakeStream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """The stack of handles that torch's current stream would be; starts on 1."""
+    stack = [1]
+
+    @contextlib.contextmanager
+    def on(stream):
+        stack.append(stream.cuda_stream)
+        yield
+        stack.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: FakeStream(h))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: FakeStream(stack[-1]))
+    monkeypatch.setattr(api, "_current_stream", lambda dev: stack[-1])
+    monkeypatch.setattr(api, "_cuda", lambda name, t: 0)
+    return stack
+
+
+class Recorder:
+    """A layer on the CPU whose kernel only notes on which stream it was called,
+    and whose workspace notes on which it was allocated."""
+
+    def __init__(self, monkeypatch, stack):
+        self.allocated, self.ran, self.recorded = [], [], []
+        prob = api.make_problem(2, 16, 4, 2, 16)
+        self.layer = MoeLayer(prob, {"w13": None, "w2": None}, "cpu")
+        self.layer._check_weights = lambda: None
+        rec = self
+
+        class Workspace:
+            def record_stream(self, s):
+                rec.recorded.append(s.cuda_stream)
+
+        def alloc(prob, device):
+            rec.allocated.append(stack[-1])
+            return Workspace()
+
+        monkeypatch.setattr(api, "alloc_few_workspace", alloc)
+        self.layer._forward_few = lambda prob, x, w, y, r, stats, ws, stream: rec.ran.append(
+            stack[-1] if stream is None else api._stream(stream))
+        self.x = torch.zeros((2, 16), dtype=torch.bfloat16)
+
+    def call(self, stream=None):
+        self.layer.forward_few(self.x, torch.empty_like(self.x), stream=stream)
+
+
+@pytest.mark.parametrize("stream", [FakeStream(7), 7])
+def test_the_few_token_workspace_is_cleared_on_the_stream_that_uses_it(streams, monkeypatch, stream):
+    r = Recorder(monkeypatch, streams)
+    r.call(stream)
+    assert r.allocated == r.ran == [7] and streams == [1]
+    r.call(stream)
+    assert r.allocated == [7] and r.recorded == []       # once, and the same stream again
+    r.call()                                             # another stream: the allocator is told
+    assert r.ran == [7, 7, 1] and r.recorded == [1]
+
+
+def test_the_few_token_workspace_on_the_current_stream(streams, monkeypatch):
+    r = Recorder(monkeypatch, streams)
+    r.call()
+    r.call()
+    assert r.allocated == [1] and r.ran == [1, 1] and r.recorded == []
+    r.call(9)
+    assert r.recorded == [9]
+
+
+def test_no_stream_context_without_a_stream(streams):
+    with api._on_stream(None, 0):
+        assert streams == [1]
+    with api._on_stream(3, 0):
+        assert streams == [1, 3]
