@@ -300,6 +300,18 @@ def _on_stream(stream, dev: int):
     return torch.cuda.stream(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor for a kernel on `stream` to write: from that stream's memory,
+    which no pending work of another stream uses.  It may be read on the current
+    stream and freed without waiting for either (the allocator knows both)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on_stream(stream, torch.device(device).index):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _enqueue(name: str, dev: int, stream, *args) -> None:
     """Call the C entry point `name` with args and the stream handle (`stream`,
     or device dev's current stream), device dev being current."""
@@ -394,8 +406,9 @@ def moe_quantize_rows(x, x_q, x_scale, stream=None):
 
 def quantize_rows(x: torch.Tensor, stream=None) -> tuple:
     """(x_q, x_scale) of moe_quantize_rows in new tensors."""
-    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-    s = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _cuda("x", x)
+    q = _empty(x.shape, torch.int8, x.device, stream)
+    s = _empty(x.shape[:-1], torch.float32, x.device, stream)
     moe_quantize_rows(x, q, s, stream)
     return q, s
 

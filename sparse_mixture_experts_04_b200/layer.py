@@ -63,7 +63,7 @@ class MoeLayer:
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, with_stats: bool = True,
                 stream=None) -> torch.Tensor:
         if y is None:
-            y = torch.empty((self.prob.T, self.prob.d_model), dtype=self.dtype, device=self.device)
+            y = api._empty((self.prob.T, self.prob.d_model), self.dtype, self.device, stream)
         self._forward(self.prob, x, self.weights, y, self.routing, self.stats if with_stats else None, self.ws, stream)
         return y
 
@@ -77,9 +77,9 @@ class MoeLayer:
         outputs keep more bits up to the combine).  Up to twice as fast for
         one token; from 32 tokens on forward() can be the faster.  No backward() from it: that reads what forward()
         leaves behind.  Its device status is in self.few_ws."""
-        if y is None:
-            y = torch.empty((self.prob.T, self.prob.d_model), dtype=self.dtype, device=self.device)
         dev = api._cuda("x", x)
+        if y is None:
+            y = api._empty((self.prob.T, self.prob.d_model), self.dtype, self.device, stream)
         handle = api._stream_handle(stream, dev)
         if self.few_ws is None:
             self._check_weights()

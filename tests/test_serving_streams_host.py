@@ -85,3 +85,33 @@ def test_no_stream_context_without_a_stream(streams):
         assert streams == [1]
     with api._on_stream(3, 0):
         assert streams == [1, 3]
+
+
+def test_outputs_are_allocated_on_the_stream_that_writes_them(streams, monkeypatch):
+    """forward, forward_few and quantize_rows without output tensors, on a stream."""
+    made, recorded = [], []
+
+    class Out:
+        device = torch.device("cpu")
+
+        def record_stream(self, s):
+            recorded.append(s.cuda_stream)
+
+    def empty(*args, **kwargs):
+        made.append(streams[-1])
+        return Out()
+
+    r = Recorder(monkeypatch, streams)
+    r.layer._forward = lambda *a: None
+    monkeypatch.setattr(api, "moe_quantize_rows", lambda *a: None)
+    monkeypatch.setattr(torch, "empty", empty)
+    for call, n in ((lambda s: r.layer.forward_few(r.x, stream=s), 1), (lambda s: r.layer.forward(r.x, stream=s), 1),
+                    (lambda s: api.quantize_rows(r.x, stream=s), 2)):
+        made.clear()
+        recorded.clear()
+        call(5)
+        assert made == [5] * n and recorded == [1] * n   # written on 5, read on the current one
+        made.clear()
+        recorded.clear()
+        call(None)
+        assert made == [1] * n and recorded == []
