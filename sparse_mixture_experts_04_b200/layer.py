@@ -40,6 +40,7 @@ class MoeLayer:
             weights["expert_capacity"] = torch.full((E,), cap, dtype=torch.int32, device=self.device)
         self._balance_step = 0
         self._count_hist = None
+        self._last = None  # whose call left the routing arrays: "forward" or "few"
 
     @classmethod
     def from_inputs(cls, inputs: dict, device="cuda", flags: int = 0, keep_routing: bool = True) -> "MoeLayer":
@@ -65,6 +66,7 @@ class MoeLayer:
         if y is None:
             y = api._empty((self.prob.T, self.prob.d_model), self.dtype, self.device, stream)
         self._forward(self.prob, x, self.weights, y, self.routing, self.stats if with_stats else None, self.ws, stream)
+        self._last = "forward"
         return y
 
     __call__ = forward
@@ -75,8 +77,14 @@ class MoeLayer:
         tokens (decode steps): same inputs, outputs, routing and statistics.
         Agrees with forward() to rounding (hidden activations and expert
         outputs keep more bits up to the combine).  Up to twice as fast for
-        one token; from 32 tokens on forward() can be the faster.  No backward() from it: that reads what forward()
-        leaves behind.  Its device status is in self.few_ws."""
+        one token; from 32 tokens on forward() can be the faster.
+
+        No backward() from it: that reads what forward() leaves behind, and the
+        routing arrays (self.routing) belong to both.  backward() refuses until
+        the next forward(); a replayed graph of this call overwrites them unseen,
+        so replay none between forward() and backward().  A layer built with
+        keep_routing=False has no such arrays, and a pending backward() stays
+        good.  Its device status is in self.few_ws."""
         dev = api._cuda("x", x)
         if y is None:
             y = api._empty((self.prob.T, self.prob.d_model), self.dtype, self.device, stream)
@@ -91,6 +99,8 @@ class MoeLayer:
                 self.few_ws.record_stream(torch.cuda.current_stream(dev))
         self._forward_few(self.prob, x, self.weights, y, self.routing, self.stats if with_stats else None,
                           self.few_ws, handle)
+        if self.routing is not None or self._last is None:
+            self._last = "few"
         return y
 
     def _weight_shapes(self) -> dict:
@@ -145,13 +155,18 @@ class MoeLayer:
         if x is not None:
             self.graph_x.copy_(x)
         self._graph.replay()
+        self._last = "forward"
         return self.graph_y
 
     def backward(self, x: torch.Tensor, dy: torch.Tensor, d_loss: float = 1.0, d_zloss: float = 0.0,
                  stream=None) -> dict:
-        """Gradients of the last forward (same x; the workspace untouched since),
-        for dJ/dy = dy and dJ/d(balance loss) = d_loss, dJ/d(z-loss) = d_zloss.
-        Returns FP32 weight gradients and dx (activation dtype)."""
+        """Gradients of the last forward (same x; the workspace and the routing
+        arrays untouched since), for dJ/dy = dy and dJ/d(balance loss) = d_loss,
+        dJ/d(z-loss) = d_zloss.  Returns FP32 weight gradients and dx (activation
+        dtype).  RuntimeError after forward_few(), which overwrites the routing."""
+        if self._last == "few":
+            raise RuntimeError("backward() needs a forward() of the same x: forward_few() was the last call, and it "
+                               "leaves no activations and another routing")
         P, dev = self.prob, self.device
         f32 = dict(dtype=torch.float32, device=dev)
         E, d, F, Ns, T = P.n_experts, P.d_model, P.d_ff, P.n_shared, P.T
@@ -236,6 +251,7 @@ class MoeLayer:
                 if stats_host is not None:
                     stats_host[i].copy_(sb[b], non_blocking=True)
                 copied_out[i].record(d2h)
+        self._last = "forward"
         comp.wait_stream(d2h)
         comp.synchronize()
 

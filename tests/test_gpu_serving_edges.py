@@ -4,7 +4,7 @@ limits."""
 import pytest
 import torch
 
-from sparse_mixture_experts_04_b200 import api
+from sparse_mixture_experts_04_b200 import MoeLayer, api
 from test_gpu_few import build, make
 
 pytestmark = pytest.mark.gpu
@@ -58,3 +58,28 @@ def test_new_outputs_on_a_side_stream_keep_their_values():
         torch.cuda.synchronize()
         assert torch.equal(y, want) and torch.equal(z, want_fwd)
         assert torch.equal(q, want_q) and torch.equal(s, want_s)
+
+
+def test_a_few_token_call_between_forward_and_backward():
+    """With routing arrays backward() refuses; without, the pending gradients are
+    those of the forward alone, bit for bit."""
+    T, d, E, K, F, Ns = 24, 128, 8, 2, 128, 1
+    inp = make(T, d, E, K, F, Ns, "bf16", 33)
+    x, other = inp["x"].cuda(), inp["x"].flip(0).cuda().contiguous()
+    dy = torch.randn((T, d), generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    w = {k: torch.as_tensor(v).cuda() for k, v in inp.items() if k != "x" and v is not None}
+    prob = api.make_problem(T, d, E, K, F, Ns, 1.0, "bf16", 0, 0.01)
+    plain = MoeLayer(prob, w)
+    plain.forward(x)
+    want = {k: v.clone() for k, v in plain.backward(x, dy).items()}
+    plain.forward_few(other)
+    with pytest.raises(RuntimeError):
+        plain.backward(x, dy)
+    plain.forward(x)
+    again = plain.backward(x, dy)
+    bare = MoeLayer(prob, w, keep_routing=False)
+    bare.forward(x)
+    bare.forward_few(other)
+    got = bare.backward(x, dy)
+    for k, v in want.items():
+        assert torch.equal(again[k], v) and torch.equal(got[k], v), k
