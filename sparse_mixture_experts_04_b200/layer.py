@@ -258,11 +258,14 @@ class MoeLayer:
 
 def quantize_weights(weights: dict) -> dict:
     """The weights of a layer (w13, w2 and the shared ones, BF16 or FP32, on a
-    CUDA device) to 8 bits with a scale per output channel, for MoeLayerI8; the
-    router's arrays and expert_capacity are passed on.  The shared experts are
+    CUDA device) to 8 bits with a scale per output channel, for MoeLayerI8.
+    w_gate and logit_offset are passed on; sel_bias and expert_capacity, which
+    balance_update() writes, are copied.  The shared experts are
     one expert of width N_s * F: w2_shared has one scale per output channel
     over all of them."""
-    out = {k: weights.get(k) for k in ("w_gate", "logit_offset", "sel_bias", "expert_capacity")}
+    out = {k: weights.get(k) for k in ("w_gate", "logit_offset")}
+    for k in ("sel_bias", "expert_capacity"):
+        out[k] = None if weights.get(k) is None else weights[k].clone()
     for k in ("w13", "w2", "w13_shared"):
         if weights.get(k) is not None:
             out[k], out[k + "_scale"] = api.quantize_rows(weights[k])
@@ -303,7 +306,8 @@ class MoeLayerI8(MoeLayer):
 
     @classmethod
     def from_layer(cls, layer: MoeLayer, keep_routing: bool = True) -> "MoeLayerI8":
-        """Quantise an existing layer's weights (the layer keeps its own)."""
+        """Quantise an existing layer's weights.  The layer keeps its own; both
+        adapt apart from each other (balance_update), from the same start."""
         return cls(layer.prob, quantize_weights(layer.weights), layer.device, keep_routing)
 
     @classmethod

@@ -4,7 +4,7 @@ limits."""
 import pytest
 import torch
 
-from sparse_mixture_experts_04_b200 import MoeLayer, api
+from sparse_mixture_experts_04_b200 import MoeLayer, MoeLayerI8, api
 from test_gpu_few import build, make
 
 pytestmark = pytest.mark.gpu
@@ -83,3 +83,19 @@ def test_a_few_token_call_between_forward_and_backward():
     got = bare.backward(x, dy)
     for k, v in want.items():
         assert torch.equal(again[k], v) and torch.equal(got[k], v), k
+
+
+def test_balance_update_of_the_8bit_layer_leaves_its_source_alone():
+    T, E = 48, 6
+    inp = make(T, 64, E, 2, 48, 0, "bf16", 34, bias=0.1)
+    base = build(inp, 2, 1.0, api.FLAG_EXPERT_CAPACITY)
+    small = MoeLayerI8.from_layer(base)
+    x = inp["x"].cuda()
+    before = {k: base.weights[k].clone() for k in ("sel_bias", "expert_capacity")}
+    first = base.forward_few(x).clone()
+    for _ in range(2):
+        small.forward_few(x)
+        small.balance_update(bias_rate=0.05, c_base=0.9, gamma=0.5)
+    for k, v in before.items():
+        assert torch.equal(base.weights[k], v) and not torch.equal(small.weights[k], v), k
+    assert torch.equal(base.forward_few(x), first)

@@ -3,7 +3,8 @@ or kept apart (no GPU: the entry points are stand-ins)."""
 import pytest
 import torch
 
-from sparse_mixture_experts_04_b200 import MoeLayer, api
+import serving_ref as ref
+from sparse_mixture_experts_04_b200 import MoeLayer, MoeLayerI8, api, quantize_weights
 
 
 @pytest.fixture
@@ -62,3 +63,27 @@ def test_a_replayed_forward_counts_as_one(layer):
     m.forward_few(X)
     m.forward_graphed()
     m.backward(X, X)
+
+
+# ------------------------------------------------------- a layer and its 8-bit copy
+@pytest.fixture
+def quantisable(monkeypatch):
+    """quantize_weights and MoeLayerI8 on CPU tensors, with the 64-bit rule."""
+    monkeypatch.setattr(api, "quantize_rows", lambda x: (lambda q, s: (q.to(torch.int8), s.float()))(*ref.quantize(x)))
+    monkeypatch.setattr(MoeLayerI8, "_check_weights", lambda self: None)
+    g = torch.Generator().manual_seed(2)
+    bf = lambda *shape: torch.randn(shape, generator=g).bfloat16()
+    return dict(w_gate=bf(4, 16), w13=bf(4, 32, 16), w2=bf(4, 16, 16), sel_bias=torch.zeros(4), logit_offset=None)
+
+
+def test_the_8bit_layer_adapts_on_its_own(quantisable):
+    base = MoeLayer(api.make_problem(2, 16, 4, 2, 16, 0, 1.0, flags=api.FLAG_EXPERT_CAPACITY), quantisable, "cpu")
+    small = MoeLayerI8.from_layer(base)
+    for k in ("sel_bias", "expert_capacity"):
+        assert torch.equal(small.weights[k], base.weights[k])
+        before = base.weights[k].clone()
+        small.weights[k].add_(1)          # as balance_update does, in place
+        assert torch.equal(base.weights[k], before), k
+        base.weights[k].sub_(1)
+        assert torch.equal(small.weights[k], before + 1), k
+    assert quantize_weights({k: v for k, v in quantisable.items() if k != "sel_bias"})["sel_bias"] is None
