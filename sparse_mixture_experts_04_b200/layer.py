@@ -307,8 +307,11 @@ class MoeLayerI8(MoeLayer):
     @classmethod
     def from_layer(cls, layer: MoeLayer, keep_routing: bool = True) -> "MoeLayerI8":
         """Quantise an existing layer's weights.  The layer keeps its own; both
-        adapt apart from each other (balance_update), from the same start."""
-        return cls(layer.prob, quantize_weights(layer.weights), layer.device, keep_routing)
+        adapt apart from each other (balance_update), from the same start.
+        FLAG_SAVE_GU, which serves the backward, is dropped."""
+        prob = type(layer.prob).from_buffer_copy(layer.prob)
+        prob.flags &= ~api.FLAG_SAVE_GU
+        return cls(prob, quantize_weights(layer.weights), layer.device, keep_routing)
 
     @classmethod
     def from_inputs(cls, inputs: dict, device="cuda", flags: int = 0, keep_routing: bool = True) -> "MoeLayerI8":

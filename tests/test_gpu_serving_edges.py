@@ -99,3 +99,14 @@ def test_balance_update_of_the_8bit_layer_leaves_its_source_alone():
     for k, v in before.items():
         assert torch.equal(base.weights[k], v) and not torch.equal(small.weights[k], v), k
     assert torch.equal(base.forward_few(x), first)
+
+
+def test_a_training_layer_and_its_8bit_copy():
+    """FLAG_SAVE_GU has no meaning for the copy, which equals the one made of the
+    same layer without the flag."""
+    inp = make(20, 64, 6, 2, 48, 1, "bf16", 35)
+    x = inp["x"].cuda()
+    a = MoeLayerI8.from_layer(build(inp, 2, 1.0, api.FLAG_SAVE_GU, None, 1))
+    b = MoeLayerI8.from_layer(build(inp, 2, 1.0, 0, None, 1))
+    assert torch.equal(a.forward(x), b.forward(x)) and torch.equal(a.forward_few(x), b.forward_few(x))
+    assert api.read_device_status(a.ws) == 0 and api.read_device_status(a.few_ws) == 0

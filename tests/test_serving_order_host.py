@@ -87,3 +87,11 @@ def test_the_8bit_layer_adapts_on_its_own(quantisable):
         base.weights[k].sub_(1)
         assert torch.equal(small.weights[k], before + 1), k
     assert quantize_weights({k: v for k, v in quantisable.items() if k != "sel_bias"})["sel_bias"] is None
+
+
+def test_a_training_layer_can_be_quantised(quantisable):
+    flags = api.FLAG_SAVE_GU | api.FLAG_EXTENDED_STATS
+    base = MoeLayer(api.make_problem(2, 16, 4, 2, 16, flags=flags), quantisable, "cpu")
+    small = MoeLayerI8.from_layer(base)
+    assert small.prob.flags == api.FLAG_EXTENDED_STATS and base.prob.flags == flags
+    assert small.stats.shape == base.stats.shape
