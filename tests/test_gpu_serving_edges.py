@@ -1,11 +1,16 @@
 """Calls of the serving operators that their documents allow and that are easy to
 get wrong: first calls on a side stream, forwards in other orders, sizes at the
 limits."""
+import importlib.util
+import os
+
 import pytest
 import torch
 
+import serving_ref as ref
 from sparse_mixture_experts_04_b200 import MoeLayer, MoeLayerI8, api
 from test_gpu_few import build, make
+from test_quant_rule_host import rows_of_every_bf16_maximum
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +115,21 @@ def test_a_training_layer_and_its_8bit_copy():
     b = MoeLayerI8.from_layer(build(inp, 2, 1.0, 0, None, 1))
     assert torch.equal(a.forward(x), b.forward(x)) and torch.equal(a.forward_few(x), b.forward_few(x))
     assert api.read_device_status(a.ws) == 0 and api.read_device_status(a.few_ws) == 0
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_one_scale_rule_everywhere(dt):
+    """moe_quantize_rows, the 64-bit form of the tests, elementary torch operations
+    on the GPU and the measured cases' plain form: one rule, bit for bit."""
+    spec = importlib.util.spec_from_file_location(
+        "measured_cases", os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "perf", "operators.py"))
+    cases = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(cases)
+    x = rows_of_every_bf16_maximum().to(dt).cuda()
+    q, s = api.quantize_rows(x)
+    wq, ws = ref.quantize(x.cpu())
+    assert torch.equal(s.cpu().double(), ws) and torch.equal(q.cpu().double(), wq)
+    t = x.float().abs().amax(1) / 127.0
+    assert torch.equal(s, t) and torch.equal(q.double(), torch.round(x.double() / t.double()[:, None]))
+    pq, ps = cases._quantize(x)
+    assert torch.equal(q.float(), pq) and torch.equal(s, ps)
