@@ -8,8 +8,9 @@ import pytest
 import torch
 
 import serving_ref as ref
+import test_gpu_few
 from sparse_mixture_experts_04_b200 import MoeLayer, MoeLayerI8, api
-from test_gpu_few import build, make
+from test_gpu_few import build, make, run
 from test_quant_rule_host import rows_of_every_bf16_maximum
 
 pytestmark = pytest.mark.gpu
@@ -133,3 +134,93 @@ def test_one_scale_rule_everywhere(dt):
     assert torch.equal(s, t) and torch.equal(q.double(), torch.round(x.double() / t.double()[:, None]))
     pq, ps = cases._quantize(x)
     assert torch.equal(q.float(), pq) and torch.equal(s, ps)
+
+
+# ------------------------------------------------------------ sizes at the limits
+@pytest.fixture
+def wide_router(monkeypatch):
+    """exact_router_inputs for rows of more than 4096: the columns beyond have no say
+    in the routing (gate weights of zero), so the logits stay exact."""
+    exact = test_gpu_few.exact_router_inputs
+
+    def inputs(T, d, E, seed):
+        inp = exact(T, min(d, 4096), E, seed)
+        if d > 4096:
+            more = torch.randn((T, d - 4096), generator=torch.Generator().manual_seed(seed + d))
+            inp["x"] = torch.cat([inp["x"].float(), more], 1)
+            inp["w_gate"] = torch.cat([inp["w_gate"].float(), torch.zeros((E, d - 4096))], 1)
+        return inp
+
+    monkeypatch.setattr(test_gpu_few, "exact_router_inputs", inputs)
+
+
+@pytest.mark.parametrize("T,d,E,K,F,Ns,C", [
+    (64, 4096, 2, 1, 4120, 1, 0.0),     # 32 rows per expert: groups of 16, three uneven chunks of the reduction
+    (33, 4096, 2, 2, 4104, 0, 0.0),     # groups of 16, 16 and 1
+    (48, 2816, 3, 2, 2072, 2, 0.75),    # chunks of one and a half stages, a capacity
+    (61, 6144, 2, 1, 2056, 1, 0.0),
+])
+def test_few_layer_of_wide_rows_and_many_tokens(T, d, E, K, F, Ns, C, wide_router):
+    """BF16 rows of more than 4 KB with more than 8 rows per expert (token groups
+    of up to 16 rows, 32 with the hidden rows' low parts)."""
+    run(T, d, E, K, F, Ns, "bf16", C)
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 34784), ("f32", 17392), ("i8", 69568)])
+@pytest.mark.parametrize("T", [1, 5])
+def test_few_layer_of_the_widest_rows(T, kind, d, wide_router):
+    run(T, d, 2, 1, 16, 1, kind)
+
+
+@pytest.mark.parametrize("kind,F", [("bf16", 40008), ("f32", 20008), ("i8", 69584)])
+def test_few_layer_of_long_reductions(kind, F):
+    """Down products of ten chunks and more."""
+    run(5, 64, 2, 1, F, 1, kind)
+
+
+def quantize_check(x, q, s):
+    """Rows against elementary operations on the GPU, a few at a time."""
+    inv = torch.tensor(1.0 / 127.0, dtype=torch.float32, device="cuda")
+    step = max(1, (1 << 26) // x.shape[1])
+    for a in range(0, len(x), step):
+        v = x[a:a + step]
+        t = (v.float().abs().amax(1) * inv).clamp_(min=2.0 ** -126)
+        assert torch.equal(s[a:a + step], t), a
+        assert torch.equal(q[a:a + step].double(), torch.round(v.double() / t.double()[:, None])), a
+
+
+@pytest.mark.parametrize("rows,cols,dt", [
+    (524288 + 777, 16, torch.bfloat16), (262144 + 333, 2064, torch.bfloat16), (131072 + 333, 4112, torch.bfloat16),
+    (65536 + 333, 8208, torch.bfloat16), (65536 + 33, 16400, torch.bfloat16), (262144 + 333, 1040, torch.float32)])
+def test_quantize_more_rows_than_a_grid_holds(rows, cols, dt):
+    """One, two, four and eight warps per row and a block per row, more than once around."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.empty((rows, cols), dtype=dt, device="cuda").normal_(generator=g)
+    x *= torch.rand((rows, 1), device="cuda", generator=g).to(dt) + 0.01   # neighbours have other maxima
+    quantize_check(x, *api.quantize_rows(x))
+
+
+@pytest.mark.parametrize("T,d,Ns", [(524288 + 777, 64, 1), (262144 + 333, 2064, 0)])
+def test_8bit_layer_of_more_tokens_than_a_grid_holds(T, d, Ns):
+    """Every token's output equals the one that a layer of its own gives, bit for
+    bit: integer sums are exact, and the roundings do not depend on the tile."""
+    E, K, F = 4, 2, 16
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rnd = lambda *sh: torch.empty(sh, device="cuda").normal_(generator=g)
+    i8 = lambda *sh: torch.randint(-127, 128, sh, dtype=torch.int8, device="cuda", generator=g)
+    w = dict(w13=i8(E, 2 * F, d), w13_scale=rnd(E, 2 * F).abs() / d, w2=i8(E, d, F), w2_scale=rnd(E, d).abs() / F)
+    if Ns:
+        w.update(w13_shared=i8(Ns, 2 * F, d), w13_shared_scale=rnd(Ns, 2 * F).abs() / d, w2_shared=i8(Ns, d, F),
+                 w2_shared_scale=rnd(d).abs() / F)
+    x, logits = rnd(T, d).bfloat16(), rnd(T, E)
+
+    def forward(a, b):
+        layer = MoeLayerI8(api.make_problem(b - a, d, E, K, F, Ns, flags=api.FLAG_LOGITS_GIVEN), w)
+        layer.routing["logits"].copy_(logits[a:b])
+        y = layer.forward(x[a:b], with_stats=False)
+        assert api.read_device_status(layer.ws) == 0
+        return y
+
+    y = forward(0, T)
+    for a in (0, T // 2, T - 900):
+        assert torch.equal(y[a:a + 900], forward(a, a + 900)), a
