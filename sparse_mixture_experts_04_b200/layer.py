@@ -115,18 +115,22 @@ class MoeLayer:
         return out
 
     def _check_weights(self) -> None:
-        """Raise ValueError unless the weights have the problem's shapes and types."""
+        """Raise ValueError unless the weights have the problem's shapes and types and
+        are on the layer's device."""
         E = self.prob.n_experts
         for name, (shape, dtype) in self._weight_shapes().items():
             t = self.weights.get(name)
-            if t is None or tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"weights['{name}'] must be a contiguous CUDA {dtype} tensor of shape {shape}")
+            if (t is None or tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or
+                    t.device != self.ws.device):
+                raise ValueError(f"weights['{name}'] must be a contiguous CUDA {dtype} tensor of shape {shape} on the "
+                                 "layer's device")
         for name, dtype in (("logit_offset", torch.float32), ("sel_bias", torch.float32),
                             ("expert_capacity", torch.int32)):
             t = self.weights.get(name)
             if t is not None and (tuple(t.shape) != (E,) or t.dtype != dtype or not t.is_cuda or
-                                  not t.is_contiguous()):
-                raise ValueError(f"weights['{name}'] must be a contiguous CUDA {dtype} tensor of shape {(E,)}")
+                                  not t.is_contiguous() or t.device != self.ws.device):
+                raise ValueError(f"weights['{name}'] must be a contiguous CUDA {dtype} tensor of shape {(E,)} on the "
+                                 "layer's device")
 
     def capture(self, with_stats: bool = True) -> None:
         """Capture one forward into a CUDA graph over static input/output

@@ -95,3 +95,30 @@ def test_a_training_layer_can_be_quantised(quantisable):
     small = MoeLayerI8.from_layer(base)
     assert small.prob.flags == api.FLAG_EXTENDED_STATS and base.prob.flags == flags
     assert small.stats.shape == base.stats.shape
+
+
+# ------------------------------------------------------------------------ devices
+class OnDevice:
+    """A contiguous CUDA tensor as far as a check of its properties goes."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, index):
+        self.shape, self.dtype, self.device = shape, dtype, torch.device("cuda", index)
+
+    def is_contiguous(self):
+        return True
+
+
+@pytest.mark.parametrize("cls", [MoeLayer, MoeLayerI8])
+def test_weights_on_another_device_are_refused(cls):
+    layer = cls.__new__(cls)
+    layer.prob, layer.dtype = api.make_problem(2, 32, 4, 2, 16, 1), torch.bfloat16
+    layer.ws = OnDevice((1,), torch.uint8, 1)
+    good = {k: OnDevice(shape, dtype, 1) for k, (shape, dtype) in layer._weight_shapes().items()}
+    good["sel_bias"] = OnDevice((4,), torch.float32, 1)
+    layer.weights = good
+    layer._check_weights()
+    for k, t in good.items():
+        layer.weights = dict(good, **{k: OnDevice(t.shape, t.dtype, 0)})
+        with pytest.raises(ValueError, match=k):
+            layer._check_weights()
