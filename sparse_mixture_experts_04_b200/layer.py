@@ -21,7 +21,7 @@ class MoeLayer:
         self.weights = weights
         self.ws = self._alloc_workspace(prob, self.device)
         self.few_ws = None  # forward_few's workspace, allocated by its first call on that call's stream
-        self._few_stream = None
+        self._few_streams = set()  # handles of the streams that have used it
         self.dtype = torch.bfloat16 if prob.dtype == api.DTYPE_BF16 else torch.float32
         T, E, K = prob.T, prob.n_experts, prob.top_k
         self.routing = None
@@ -93,10 +93,11 @@ class MoeLayer:
             self._check_weights()
             with api._on_stream(stream, dev):  # its clearing runs in front of the kernel, on the same stream
                 self.few_ws = api.alloc_few_workspace(self.prob, self.device)
-            self._few_stream = handle
-        elif handle != self._few_stream:  # freed while this stream still uses it, it is not handed out again
+            self._few_streams = {handle}
+        elif handle not in self._few_streams:  # freed while this stream still uses it, it is not handed out again
             with api._on_stream(stream, dev):
                 self.few_ws.record_stream(torch.cuda.current_stream(dev))
+            self._few_streams.add(handle)
         self._forward_few(self.prob, x, self.weights, y, self.routing, self.stats if with_stats else None,
                           self.few_ws, handle)
         if self.routing is not None or self._last is None:

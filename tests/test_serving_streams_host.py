@@ -77,7 +77,9 @@ def test_the_few_token_workspace_on_the_current_stream(streams, monkeypatch):
     r.call()
     assert r.allocated == [1] and r.ran == [1, 1] and r.recorded == []
     r.call(9)
-    assert r.recorded == [9]
+    r.call(9)
+    r.call()
+    assert r.recorded == [9]                              # once for each stream
 
 
 def test_no_stream_context_without_a_stream(streams):
