@@ -1428,14 +1428,20 @@ cudaError_t launch_few_layer(const Problem& p, const FewCall& c, cudaStream_t st
   a.stall_ns = test_stall_ns();
   few_tiling(p, c.i8, FewTile<kFewBF16>::kTokBytes, &a);
   // BF16 rows of more than 4 KB: 16 rows fit the token buffer only with half the
-  // ring.  Taken when that saves a tenth of the reads (d = 4096, E = 8,
-  // F = 14336, top-2: 48 tokens 825 -> 580 us, 64 tokens 1024 -> 755 us; measured
-  // before the hidden rows got their low parts).
+  // ring, whose stream is some 15% slower.  Taken when that saves 23% of the reads;
+  // us without / with it, by the share of the reads that is left:
+  //   0.58  d = 6144, E = 8,  F = 8192,  top-2,     64 tokens  1165 / 879
+  //   0.60  d = 4096, E = 8,  F = 14336, top-2,     64 tokens   952 / 767
+  //   0.67  the same,                               32 tokens   591 / 563
+  //   0.75  d = 2816, E = 16, F = 5632,  top-2 + 1, 64 tokens   437 / 419
+  //   0.79  d = 4096, E = 16, F = 4096,  top-2 + 2, 40 tokens   417 / 430
+  //   0.80  d = 4096, E = 8,  F = 14336, top-2,     24 tokens   484 / 561
+  //   0.98  d = 4096, E = 128, F = 1536, top-8 + 1, 64 tokens   825 / 945
   bool many = false;
   if (!c.i8 && p.dtype == kBF16) {
     FewArgs m = a;
     few_tiling(p, false, FewTile<kFewBF16Many>::kTokBytes, &m);
-    if (few_reads(p, m) < 0.9 * few_reads(p, a)) {
+    if (few_reads(p, m) < 0.77 * few_reads(p, a)) {
       a = m;
       many = true;
     }

@@ -159,6 +159,7 @@ def wide_router(monkeypatch):
     (33, 4096, 2, 2, 4104, 0, 0.0),     # groups of 16, 16 and 1
     (48, 2816, 3, 2, 2072, 2, 0.75),    # chunks of one and a half stages, a capacity
     (61, 6144, 2, 1, 2056, 1, 0.0),
+    (60, 4096, 3, 2, 2072, 2, 0.75),
 ])
 def test_few_layer_of_wide_rows_and_many_tokens(T, d, E, K, F, Ns, C, wide_router):
     """BF16 rows of more than 4 KB with more than 8 rows per expert (token groups
