@@ -397,9 +397,13 @@ int moe_layer_backward(const moe_problem_t* p, const void* x, const moe_weights_
  *     status word is its first word, as everywhere, and is reset by the call;
  *   - logits are summed in FP32 and FP64, expert outputs stay in FP32 up to
  *     the combine and hidden activations keep 16 bits or more
- *     (moe_layer_forward rounds both to the activations' type), so the two
- *     entry points agree to rounding, not bit for bit.
+ *     (moe_layer_forward rounds both to the activations' type), so logits and
+ *     outputs of the two entry points agree to rounding, not bit for bit.  Where
+ *     two experts' scores lie closer together than that rounding, the two may
+ *     choose different ones: the same choice is only sure with the logits given.
  *     Results of one entry point repeat bit for bit;
+ *   - after a bounded wait was given up (MOE_DEV_WAIT_TIMEOUT) y and the routing
+ *     outputs may be written in part or not at all;
  *   - MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_TOKENS, or a d_model whose row
  *     of weights exceeds 69568 bytes (34784 for BF16, 17392 for FP32, 69568
  *     for 8-bit weights);

@@ -2144,7 +2144,9 @@ static bool i8_single_problem(const I8Gemm& g, bool swiglu, int bn, SingleProble
 // CTAs 125 / 137 / 183 us against 162 / 199 / 201 us on pairs at 64 / 128 / 255
 // rows per expert).  Single CTAs: 256 B rows per tile, or 64 where 256 would
 // leave SMs without a tile (one row, K = 2048, N = 2816: 11 tiles 9.9 us, 44 tiles
-// 8.8 us).
+// 8.8 us).  Two problems in one launch take 256: with 64 the layer with 8-bit
+// experts and a shared one takes 98 instead of 78 us (one token, d = F = 4096, E = 8)
+// and 115 instead of 84 (d = 4096, E = 128, F = 1536).
 enum { kI8Narrow = 0, kI8Single = 1, kI8Pair = 2 };
 
 static int i8_shape(const I8Gemm& g, bool swiglu) {

@@ -27,10 +27,16 @@
 // tensor-core instructions (16 weight rows, 8 tokens).  Two teams of 4 warps
 // take a unit each; the warps of a team take 64-byte slices of the reduction in
 // turn, and their 16 x 8 sums are added in shared memory in warp order.  The
-// tensor cores are nearly idle (a stage of 32 KB arrives in 1400 cycles and is
-// multiplied in some 500), which is why the simple warp-level instruction is
-// used and not tcgen05: its 128-row tiles would be 1..8 rows full.  FP32
-// weights take fused multiply-adds (8 rows x 8 tokens per lane).  Sums are FP32
+// tensor cores are nearly idle while experts have up to 8 rows (a stage of 32 KB
+// arrives in 1400 cycles and is multiplied in some 500), so the warp-level
+// instruction does: its units of 16 weight rows spread evenly over the SMs, where a
+// tcgen05 tile takes 128 weight rows at a time.  With more rows per expert the
+// products do set the pace, and moe_layer_forward, whose tiles of few tokens have
+// 128 weight rows each as the M operand of tcgen05, is the faster (d = 4096, E = 8,
+// F = 14336, top-2: 16 tokens 471 / 430 us, 32 tokens 474 / 574, 64 tokens
+// 479 / 853, forward / this kernel).  FP32
+// weights take fused multiply-adds (8 rows x 8 tokens per lane), which read an
+// expert of more than 8 rows once per 8.  Sums are FP32
 // or int32; BF16 layers keep a hidden value as the sum of two BF16 (the tensor
 // cores' operands, 16 bits in all) and round nothing else before y.  No step
 // depends on the order in which CTAs run, so results repeat bit for bit.
