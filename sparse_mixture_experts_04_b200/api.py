@@ -296,7 +296,8 @@ def _on_stream(stream, dev: int):
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
+        handle = _stream(stream)  # (0, the default stream, is no handle that ExternalStream takes)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
     return torch.cuda.stream(stream)
 
 

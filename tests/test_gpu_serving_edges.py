@@ -46,6 +46,21 @@ def test_first_few_token_call_on_a_side_stream(kind):
     assert torch.equal(y, want) and torch.isfinite(keep).all()
 
 
+def test_first_few_token_call_on_the_default_streams_handle():
+    """The current stream is a busy one of its own; the call names the default stream."""
+    inp = make(6, 256, 8, 2, 512, 1, "bf16", 36)
+    want = build(inp, 2, Ns=1).forward_few(inp["x"].cuda()).clone()
+    layer, x = build(inp, 2, Ns=1), inp["x"].cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        busy()
+        y = layer.forward_few(x, stream=torch.cuda.default_stream().cuda_stream)
+        torch.cuda.default_stream().synchronize()
+        assert torch.equal(y.cpu(), want.cpu())
+    torch.cuda.synchronize()
+    assert bool(layer.few_ws.any()) and torch.equal(y, want)
+
+
 def test_new_outputs_on_a_side_stream_keep_their_values():
     """Outputs made by the calls themselves, while the default stream frees and
     takes blocks of the same sizes behind pending work."""

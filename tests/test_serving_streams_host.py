@@ -25,7 +25,9 @@ def streams(monkeypatch):
         stack.pop()
 
     monkeypatch.setattr(torch.cuda, "stream", on)
-    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: FakeStream(h))
+    # torch makes a stream of its own for the handle 0
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: FakeStream(h or 99))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda dev=None: FakeStream(0))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: FakeStream(stack[-1]))
     monkeypatch.setattr(api, "_current_stream", lambda dev: stack[-1])
     monkeypatch.setattr(api, "_cuda", lambda name, t: 0)
@@ -117,3 +119,11 @@ def test_outputs_are_allocated_on_the_stream_that_writes_them(streams, monkeypat
         recorded.clear()
         call(None)
         assert made == [1] * n and recorded == []
+
+
+def test_the_default_streams_handle_means_the_default_stream(streams, monkeypatch):
+    r = Recorder(monkeypatch, streams)
+    r.call(0)                                             # from a current stream of its own (1)
+    assert r.allocated == r.ran == [0]
+    with api._on_stream(FakeStream(0), 0):
+        assert streams == [1, 0]
