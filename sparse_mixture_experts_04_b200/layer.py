@@ -184,7 +184,8 @@ class MoeLayer:
             g["dw13_shared"] = torch.empty((Ns, 2 * F, d), **f32)
             g["dw2_shared"] = torch.empty((Ns, d, F), **f32)
         if getattr(self, "_bwd_ws", None) is None:
-            self._bwd_ws = api.alloc_backward_workspace(P, dev)
+            with api._on_stream(stream, dev.index):  # its clearing runs in front of the kernels
+                self._bwd_ws = api.alloc_backward_workspace(P, dev)
         api.moe_layer_backward(P, x, self.weights, self.routing, self.ws, dy, d_loss, d_zloss, g, self._bwd_ws,
                                stream)
         return g
@@ -205,7 +206,8 @@ class MoeLayer:
         hist = None
         if caps is not None:
             if self._count_hist is None or self._count_hist.shape[0] != window:
-                self._count_hist = torch.zeros((window, self.prob.n_experts), dtype=torch.int32, device=self.device)
+                with api._on_stream(stream, self.device.index):
+                    self._count_hist = torch.zeros((window, self.prob.n_experts), dtype=torch.int32, device=self.device)
                 self._balance_step = 0
             hist = self._count_hist
         cb = self.prob.capacity_factor if c_base is None else c_base

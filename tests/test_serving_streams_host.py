@@ -127,3 +127,30 @@ def test_the_default_streams_handle_means_the_default_stream(streams, monkeypatc
     assert r.allocated == r.ran == [0]
     with api._on_stream(FakeStream(0), 0):
         assert streams == [1, 0]
+
+
+def test_backward_and_balance_update_clear_their_buffers_on_their_stream(streams, monkeypatch):
+    made = []
+    real = torch.zeros
+
+    def alloc(prob, device):
+        made.append(("ws", streams[-1]))
+        return object()
+
+    def zeros(*args, **kwargs):
+        made.append(("zeros", streams[-1]))
+        return real(*args, **kwargs)
+
+    r = Recorder(monkeypatch, streams)
+    r.layer.prob = api.make_problem(2, 16, 4, 2, 16, flags=api.FLAG_EXPERT_CAPACITY)
+    r.layer.weights["expert_capacity"] = torch.full((4,), -1, dtype=torch.int32)
+    monkeypatch.setattr(api, "alloc_backward_workspace", alloc)
+    monkeypatch.setattr(api, "moe_layer_backward", lambda *a: None)
+    monkeypatch.setattr(api, "moe_balance_update", lambda *a: None)
+    r.layer.backward(r.x, r.x, stream=6)
+    assert made == [("ws", 6)]
+    monkeypatch.setattr(torch, "zeros", zeros)
+    r.layer.balance_update(stream=8)
+    assert made[1:] == [("zeros", 8)]
+    r.layer.balance_update(stream=8)
+    assert len(made) == 2 and streams == [1]
